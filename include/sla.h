@@ -35,7 +35,7 @@
  *   - Work is enqueued on the caller's stream; calls return before it runs.
  *   - Argument errors are found on the host before anything is enqueued; then
  *     nothing is written. Errors found on the device (a bounded wait that ran
- *     out, a caller label outside {0,1,2}) are recorded in the workspace's
+ *     out, a caller label outside {0,1,2}, a key length outside [0, Nk]) are recorded in the workspace's
  *     error word and reported by sla_check.
  *   - No entry point throws or exits; each returns an sla_status, and
  *     sla_last_error() gives a message for the calling thread's last failure.
@@ -61,7 +61,8 @@ typedef enum {
   SLA_ERR_WORKSPACE = 3,   /* workspace missing, misaligned or too small */
   SLA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed */
   SLA_ERR_TIMEOUT = 5,     /* a device-side bounded wait ran out (reported by sla_check) */
-  SLA_ERR_BAD_MASK = 6     /* caller label outside {0,1,2} (reported by sla_check) */
+  SLA_ERR_BAD_MASK = 6,    /* caller label outside {0,1,2} (reported by sla_check) */
+  SLA_ERR_BAD_LEN = 7      /* key length outside [0, Nk] (reported by sla_check) */
 } sla_status;
 
 /* Problem shape. kh / kl: critical / negligible fractions of the KV blocks per row. */
@@ -313,7 +314,7 @@ sla_status sla_pisa_hbar(const sla_problem* p, const void* k, const void* v, flo
                          size_t ws_bytes, void* stream);
 
 /* Synchronise the stream, read and clear the workspace's device error word.
- * Returns SLA_OK, SLA_ERR_TIMEOUT or SLA_ERR_BAD_MASK (or SLA_ERR_CUDA). */
+ * Returns SLA_OK, SLA_ERR_TIMEOUT, SLA_ERR_BAD_MASK, SLA_ERR_BAD_LEN (or SLA_ERR_CUDA). */
 sla_status sla_check(void* ws, void* stream);
 
 /* The block router for callers that cannot allocate device memory.
@@ -346,6 +347,97 @@ sla_status sla_check(void* ws, void* stream);
  *     Launch failures are returned as SLA_ERR_CUDA. */
 sla_status sla_route_noalloc(const sla_problem* p, const void* q, const void* k, int8_t* mask_out,
                              int32_t* crit_idx_out, double* scores_out, void* stream);
+
+/* ------------------------------------------------------------------ rotary positions
+ *
+ * The rotation of q and k by the tokens' positions, as it comes before sla_forward, and its
+ * transpose for the gradients that sla_backward gives (no counterpart on the pages; the
+ * method attends over video tokens, whose positions have a time, a height and a width).
+ *
+ * A head's first channels are cut into one run of channels[a] channels per axis a; channels
+ * behind the last run are copied. Pair i of axis a at a token with position p_a turns by
+ *     phi = p_a * base^(-2 i / channels[a])          (formed in fp64)
+ *     y1 = x1 cos(phi) - x2 sin(phi),  y2 = x2 cos(phi) + x1 sin(phi)   (fp32, rounded once)
+ */
+
+/* Element types of the rotary calls' tensors. */
+enum { SLA_BF16 = 0, SLA_F32 = 1 };
+
+/* A [B, H, N, D] tensor on the device: channels contiguous, the other strides in elements
+ * and multiples of 16 bytes (a stride is not read where its extent is 1), ptr 16-byte
+ * aligned. So a projection's [B, N, H, D] output is passed as it lies. */
+typedef struct {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_n;
+} sla_tensor;
+
+typedef struct {
+  int n_axes;           /* 1 .. 4 */
+  int channels[4];      /* channels of each axis: even, >= 2, together at most D */
+  int grid[4];          /* with positions NULL: extent of each axis, >= 1. Token n sits at the
+                           n-th cell, the last axis fastest; tokens behind the last cell are copied */
+  int start[4];         /* with positions NULL: position of the grid's first cell on each axis */
+  const int32_t* positions;    /* device [B, N, n_axes] (or NULL: the grid) */
+  int64_t positions_stride_b;  /* elements between two sequences' positions; 0: shared by all */
+  int pairing;          /* 0: channels 2i, 2i + 1 of an axis' run; 1: channels i, i + channels[a] / 2 */
+  double base;          /* finite, > 0 */
+} sla_rotary_spec;
+
+/* Rotate q [B, Hq, N, D] and k [B, Hk, N, D] (one of Hq, Hk may be 0; its tensors are then not
+ * read) into q_out and k_out. D is 64 or 128; B at most 65535. An output may be its own input
+ * (the same pointer and strides), else the two must not overlap. One launch on `stream`.
+ * Returns SLA_ERR_INVALID_ARG / SLA_ERR_UNSUPPORTED on bad arguments (nothing enqueued),
+ * SLA_ERR_CUDA if the launch fails, else SLA_OK. */
+sla_status sla_rotary(const sla_rotary_spec* spec, int B, int Hq, int Hk, int N, int D, int type, const sla_tensor* q,
+                      const sla_tensor* q_out, const sla_tensor* k, const sla_tensor* k_out, void* stream);
+
+/* The transposed rotation (each pair turned by -phi) of the rotated tensors' gradients.
+ * Types: SLA_BF16 to SLA_BF16, SLA_F32 to SLA_F32, SLA_F32 to SLA_BF16 (in place only where
+ * the types are the same); otherwise as sla_rotary. */
+sla_status sla_rotary_backward(const sla_rotary_spec* spec, int B, int Hq, int Hk, int N, int D, int in_type,
+                               int out_type, const sla_tensor* dq, const sla_tensor* dq_out, const sla_tensor* dk,
+                               const sla_tensor* dk_out, void* stream);
+
+/* ------------------------------------------------------------------ dense attention
+ *
+ * out = softmax(scale q k^T) v over the keys that each query sees, with its own number of
+ * keys, key lengths per sequence, shared key heads and a causal mask (cross attention, token
+ * models, one new token behind a long prompt), the rows' log-sum-exp, and the gradients. The
+ * exact attention of the sparse branch over all keys; sla_forward remains the sparse one.
+ *
+ *   q, out, dO, dq  [B, H, Nq, D] bf16,   k, v, dk, dv  [B, Hk, Nk, D] bf16 (sla_tensor: any
+ *                   layout with contiguous channels; strides are positive where the extent is
+ *                   above 1), H a multiple of Hk: query head h reads key head h / (H / Hk)
+ *   lse             [B, H, Nq] fp32, contiguous: ln sum_j e^(scale q.k_j)
+ *   kv_lens         device [B] int32, or NULL (every sequence has Nk keys). Keys behind a
+ *                   sequence's length may hold anything, NaN included; their gradients are 0.
+ *                   A length outside [0, Nk] is taken as the nearer end and reported by sla_check
+ *   causal          1: query i sees the keys j <= i + len - Nq (the last query sees the last key)
+ * A query that sees no key gives out = 0, lse = -inf and a zero gradient.
+ * D is 64 or 128; Nq, Nk at most 2^24; scale > 0.
+ */
+typedef struct {
+  int B, H, Hk, Nq, Nk, D;
+  int causal;  /* 0 or 1 */
+  float scale; /* finite, > 0; 1 / sqrt(D) is usual */
+} sla_attend_problem;
+
+/* Workspace bytes of sla_attend / sla_attend_backward for p; 0 if p is invalid (sla_last_error). */
+size_t sla_workspace_size_attend(const sla_attend_problem* p);
+size_t sla_workspace_size_attend_backward(const sla_attend_problem* p);
+
+/* Write out and lse. out may not overlap an input. */
+sla_status sla_attend(const sla_attend_problem* p, const sla_tensor* q, const sla_tensor* k, const sla_tensor* v,
+                      const int32_t* kv_lens, const sla_tensor* out, float* lse, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Gradients dq, dk, dv of sum(dO * out), from sla_attend's out and lse of the same p and
+ * kv_lens. The probabilities are recomputed; sums run in a fixed order (no atomics), so equal
+ * calls give equal bits. dk and dv of a shared key head sum over its query heads. */
+sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q, const sla_tensor* k,
+                               const sla_tensor* v, const sla_tensor* out, const float* lse, const sla_tensor* dO,
+                               const int32_t* kv_lens, const sla_tensor* dq, const sla_tensor* dk,
+                               const sla_tensor* dv, void* ws, size_t ws_bytes, void* stream);
 
 /* Self-test of the device-side failure path (no counterpart on the pages).
  *

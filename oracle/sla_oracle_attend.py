@@ -1,0 +1,111 @@
+"""fp64 reference of dense attention and its gradients (test infrastructure only).
+
+Row by row definition, torch float64 on whatever device the inputs lie:
+
+  s_ij = scale q_i . k_j over the keys that query i sees: j < len_b and, causal,
+         j <= i + len_b - Nq
+  lse_i = ln sum_j e^(s_ij),  P_ij = e^(s_ij - lse_i),  out_i = sum_j P_ij v_j
+  dP = dO V^T,  delta_i = dO_i . out_i,  T = P (dP - delta)
+  dQ = scale T K,  dK = scale T^T Q,  dV = P^T dO   (dK, dV summed over a key head's query heads)
+
+A query without keys: out = 0, lse = -inf, zero gradient. Keys behind len_b have zero gradients
+and are never read.
+
+``attend`` and ``gradients`` also give, per output element, how far rounding may move it in an
+implementation that rounds P, T, out and the results to bf16 once each (half a bf16 step is 2^-8 of the
+value) and holds everything else in fp32:
+
+  out: 2^-8 (sum_j P |v_j| + |out|)
+  dV:  2^-8 (sum_i P |dO_i| + |dV|)
+  dQ:  scale [2^-8 sum_j |T| |k_j| + sum_j P |k_j| e_i] + 2^-8 |dQ|
+  dK:  scale [2^-8 sum_i |T| |q_i| + sum_i P |q_i| e_i] + 2^-8 |dK|
+       with e_i = 2^-8 sum_d |dO_id| (2 |out_id| + sum_j P |v_jd|), what rounding of P and out
+       does to delta_i (which an implementation forms from the rounded out)
+  fp32: a score is off by at most (D + 2) 2^-24 scale sum_d |q_d k_d| =: u_i for the row's worst
+       key, so each P by 2 u_i + 2^-21 of itself; that factor multiplies the same sums.
+  underflow: P and T below 2^-126 (the smallest normal number of bf16 and fp32) may be flushed to
+       0, so every P and T is off by another 2^-126 at most, and a result by another 2^-126.
+
+Parity status: pinned by torch autograd of a masked softmax, by central differences, and by
+hand values for rows without keys.
+"""
+
+from __future__ import annotations
+
+import torch
+
+HALF_STEP = 2.0 ** -8  # of bf16, relative to the value
+TINY = 2.0 ** -126     # smallest normal number of bf16 and fp32
+
+
+def visible(Nq, Nk, n, causal, device):
+    j = torch.arange(Nk, device=device)[None, :]
+    keep = (j < n).expand(Nq, Nk)
+    if causal:
+        keep = keep & (j <= torch.arange(Nq, device=device)[:, None] + n - Nq)
+    return keep
+
+
+def _heads(q, k, v, kv_lens, causal, scale):
+    """(b, h, key head, q, k[:n], v[:n], P, lse, fp32 factor of the rows) of every head."""
+    B, H, Nq, D = q.shape
+    Hk, Nk = k.shape[1:3]
+    lens = [Nk] * B if kv_lens is None else [int(x) for x in kv_lens]
+    for b in range(B):
+        n = lens[b]
+        for h in range(H):
+            kh = h // (H // Hk)
+            Q, K, V = q[b, h].double(), k[b, kh, :n].double(), v[b, kh, :n].double()
+            if n == 0:
+                yield (b, h, kh, Q, K, V, torch.zeros(Nq, 0, dtype=torch.float64, device=q.device),
+                       torch.full((Nq,), -torch.inf, dtype=torch.float64, device=q.device), 0.0)
+                continue
+            S = (Q @ K.T) * scale
+            S = S.masked_fill(~visible(Nq, n, n, causal, q.device), -torch.inf)
+            lse = torch.logsumexp(S, dim=1)
+            P = torch.where(lse[:, None] == -torch.inf, 0.0, torch.exp(S - lse[:, None]))
+            worst = float((Q.nan_to_num(0.0).abs() @ K.abs().T).max()) * scale
+            yield b, h, kh, Q, K, V, P, lse, 2 * (D + 2) * 2.0 ** -24 * worst + 2.0 ** -21
+
+
+def attend(q, k, v, kv_lens=None, causal=False, scale=None):
+    """(out, lse, bound of out, bound of lse), fp64."""
+    D = q.shape[3]
+    scale = D ** -0.5 if scale is None else scale
+    out, bound = (torch.zeros(q.shape, dtype=torch.float64, device=q.device) for _ in range(2))
+    lse, lse_bound = (torch.zeros(q.shape[:3], dtype=torch.float64, device=q.device) for _ in range(2))
+    for b, h, _, Q, K, V, P, L, u in _heads(q, k, v, kv_lens, causal, scale):
+        out[b, h], lse[b, h] = P @ V, L
+        bound[b, h] = ((HALF_STEP + u) * P + TINY) @ V.abs() + HALF_STEP * out[b, h].abs() + TINY
+        lse_bound[b, h] = u + 2.0 ** -21 * (1 + L.abs().nan_to_num(posinf=0.0))
+    return out, lse, bound, lse_bound
+
+
+def gradients(q, k, v, dO, kv_lens=None, causal=False, scale=None):
+    """(dq, dk, dv, and the bound of each), fp64."""
+    D = q.shape[3]
+    scale = D ** -0.5 if scale is None else scale
+    zero = lambda x: torch.zeros(x.shape, dtype=torch.float64, device=x.device)  # noqa: E731
+    dq, dk, dv, bq, bk, bv = zero(q), zero(k), zero(v), zero(q), zero(k), zero(v)
+    for b, h, kh, Q, K, V, P, L, u in _heads(q, k, v, kv_lens, causal, scale):
+        n = K.shape[0]
+        seen = (L > -torch.inf)[:, None]
+        G = torch.where(seen, dO[b, h].double(), 0.0)
+        Q = torch.where(seen, Q, 0.0)
+        out = P @ V
+        delta = (G * out).sum(1)
+        dP = G @ V.T
+        T = P * (dP - delta[:, None])
+        dq[b, h] = scale * (T @ K)
+        dk[b, kh, :n] += scale * (T.T @ Q)
+        dv[b, kh, :n] += P.T @ G
+        e = ((HALF_STEP + u) * (G.abs() * (2 * out.abs() + P @ V.abs())).sum(1))[:, None]
+        # fp32: dP and delta are off by (D + 2) 2^-24 of their sums of magnitudes, P by u
+        fine = P * ((D + 2) * 2.0 ** -24 * (G.abs() @ V.abs().T) + u * (dP.abs() + delta.abs()[:, None]))
+        t = HALF_STEP * T.abs() + P * e + fine + TINY * (1 + (dP.abs() + delta.abs()[:, None]))
+        bq[b, h] = scale * (t @ K.abs()) + HALF_STEP * dq[b, h].abs() + TINY
+        bk[b, kh, :n] += scale * (t.T @ Q.abs())
+        bv[b, kh, :n] += ((HALF_STEP + u) * P + TINY).T @ G.abs()
+    bk += HALF_STEP * dk.abs() + TINY
+    bv += HALF_STEP * dv.abs() + TINY
+    return dq, dk, dv, bq, bk, bv

@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libsla.so")
 SLA_OK = 0
 _STATUS = {
     0: "SLA_OK", 1: "SLA_ERR_INVALID_ARG", 2: "SLA_ERR_UNSUPPORTED", 3: "SLA_ERR_WORKSPACE",
-    4: "SLA_ERR_CUDA", 5: "SLA_ERR_TIMEOUT", 6: "SLA_ERR_BAD_MASK",
+    4: "SLA_ERR_CUDA", 5: "SLA_ERR_TIMEOUT", 6: "SLA_ERR_BAD_MASK", 7: "SLA_ERR_BAD_LEN",
 }
 
 # Every symbol include/sla.h declares.
@@ -31,7 +31,8 @@ EXPORTS = ("sla_counts", "sla_workspace_size", "sla_route", "sla_kv_states", "sl
            "sla_selftest_wait_timeout", "sla_workspace_size_fp8", "sla_forward_fp8", "sla_forward_fp8_timed",
            "sla_quantize_kv", "sla_aggregate_states", "sla_forward_launches", "sla_route_variant",
            "sla_forward_variant", "sla_workspace_size_backward", "sla_backward", "sla_workspace_size_pisa",
-           "sla_forward_pisa", "sla_pisa_hbar", "sla_lowbit_codes")
+           "sla_forward_pisa", "sla_pisa_hbar", "sla_lowbit_codes", "sla_rotary", "sla_rotary_backward",
+           "sla_workspace_size_attend", "sla_workspace_size_attend_backward", "sla_attend", "sla_attend_backward")
 
 
 class SlaError(RuntimeError):
@@ -51,6 +52,26 @@ class Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int),
                 ("block_q", ctypes.c_int), ("block_kv", ctypes.c_int),
                 ("kh", ctypes.c_float), ("kl", ctypes.c_float)]
+
+
+class Tensor(ctypes.Structure):
+    """sla_tensor: a [B, H, N, D] device tensor with contiguous channels, strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class RotarySpec(ctypes.Structure):
+    """sla_rotary_spec (made by rotary_spec, which keeps the positions tensor alive)."""
+    _fields_ = [("n_axes", ctypes.c_int), ("channels", ctypes.c_int * 4), ("grid", ctypes.c_int * 4),
+                ("start", ctypes.c_int * 4), ("positions", ctypes.c_void_p), ("positions_stride_b", ctypes.c_int64),
+                ("pairing", ctypes.c_int), ("base", ctypes.c_double)]
+    positions_tensor = None
+
+
+class AttendProblem(ctypes.Structure):
+    """sla_attend_problem."""
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("Nq", ctypes.c_int),
+                ("Nk", ctypes.c_int), ("D", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -101,12 +122,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.sla_forward_variant.argtypes = [P, V, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         lib.sla_forward_launches.argtypes = [P, ctypes.c_int, ctypes.c_int]
         lib.sla_forward_launches.restype = ctypes.c_int
+        R, T, A = ctypes.POINTER(RotarySpec), ctypes.POINTER(Tensor), ctypes.POINTER(AttendProblem)
+        i = ctypes.c_int
+        lib.sla_rotary.argtypes = [R, i, i, i, i, i, i, T, T, T, T, vp]
+        lib.sla_rotary_backward.argtypes = [R, i, i, i, i, i, i, i, T, T, T, T, vp]
+        lib.sla_workspace_size_attend.argtypes = [A]
+        lib.sla_workspace_size_attend.restype = sz
+        lib.sla_workspace_size_attend_backward.argtypes = [A]
+        lib.sla_workspace_size_attend_backward.restype = sz
+        lib.sla_attend.argtypes = [A, T, T, T, vp, T, vp, vp, sz, vp]
+        lib.sla_attend_backward.argtypes = [A, T, T, T, T, vp, T, vp, T, T, T, vp, sz, vp]
         lib.sla_last_error.restype = ctypes.c_char_p
         lib.sla_version.restype = ctypes.c_char_p
         for name in ("sla_counts", "sla_route", "sla_kv_states", "sla_forward", "sla_forward_timed", "sla_check",
                      "sla_forward_fp8", "sla_forward_fp8_timed", "sla_quantize_kv", "sla_forward_pisa",
                      "sla_pisa_hbar", "sla_aggregate_states", "sla_backward", "sla_route_variant",
-                     "sla_forward_variant", "sla_lowbit_codes"):
+                     "sla_forward_variant", "sla_lowbit_codes", "sla_rotary", "sla_rotary_backward", "sla_attend",
+                     "sla_attend_backward"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -467,6 +499,218 @@ def quantize_kv(k, v, block_kv=64):
                                  _stream_handle(dev))
     _raise(st)
     return k8, v8, kexp, vexp
+
+
+def rotary_spec(axes, grid=None, positions=None, start=None, base=10000.0, pairing=0) -> RotarySpec:
+    """What rotary and rotary_backward turn by.
+
+    axes: channels of each axis (even; one to four axes, together at most D; channels behind them
+    are copied). Positions are either a grid, one extent per axis (token n at its n-th cell, the
+    last axis fastest, the first cell at `start`; tokens behind the last cell are copied), or an
+    int32 tensor [N, len(axes)] or [B, N, len(axes)]. pairing: 0 neighbouring channels, 1 the two
+    halves of an axis' channels.
+    """
+    axes = tuple(int(a) for a in axes)
+    if not 1 <= len(axes) <= 4:
+        raise ValueError(f"one to four axes, got {len(axes)}")
+    if (grid is None) == (positions is None):
+        raise ValueError("give either grid or positions")
+    spec = RotarySpec(n_axes=len(axes), pairing=int(pairing), base=float(base))
+    for a, d in enumerate(axes):
+        spec.channels[a] = d
+    if grid is not None:
+        grid = tuple(int(g) for g in grid)
+        start = tuple(int(x) for x in start) if start is not None else (0,) * len(axes)
+        if len(grid) != len(axes) or len(start) != len(axes):
+            raise ValueError(f"grid and start need one entry per axis ({len(axes)})")
+        for a in range(len(axes)):
+            spec.grid[a], spec.start[a] = grid[a], start[a]
+    else:
+        if start is not None:
+            raise ValueError("start goes with grid")
+        if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32 \
+                or positions.dim() not in (2, 3) or positions.shape[-1] != len(axes) or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 CUDA tensor [N, {len(axes)}] or [B, N, {len(axes)}]")
+        spec.positions = positions.data_ptr()
+        spec.positions_stride_b = positions.shape[-2] * len(axes) if positions.dim() == 3 else 0
+        spec.positions_tensor = positions
+    return spec
+
+
+def _check_heads(name, t, B, H, N, D, dtype, device):
+    """A [B, H, N, D] tensor whose channels are contiguous (the library checks the other strides)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != (B, H, N, D) or (D > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be {dtype} of shape {(B, H, N, D)} with contiguous channels, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _tensor(t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    s = t.stride()
+    return ctypes.byref(Tensor(t.data_ptr(), s[0], s[1], s[2]))
+
+
+def _span(t):
+    """The bytes [first, last) that a tensor's elements lie in."""
+    first = t.data_ptr()
+    return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _check_in_place(name, x, y):
+    """y is x itself, or apart from it: tensors that share part of their memory cannot be rotated."""
+    if y.data_ptr() == x.data_ptr() and y.stride() == x.stride() and y.dtype == x.dtype:
+        return
+    (a, b), (c, d) = _span(x), _span(y)
+    if a < d and c < b:
+        raise ValueError(f"{name} overlaps its input without being the same tensor")
+
+
+def _rotary_call(q, k, spec, out, dtype, names, backward):
+    if not isinstance(spec, RotarySpec):
+        raise ValueError("spec must come from rotary_spec")
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError(f"give {names[0]} or {names[1]}")
+    if not isinstance(first, torch.Tensor) or first.dim() != 4:
+        raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, D] tensors")
+    (B, _, N, D), dev, in_dtype = first.shape, first.device, first.dtype
+    if in_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{names[0]} and {names[1]} must be bf16 or fp32, got {in_dtype}")
+    dtype = in_dtype if dtype is None else dtype
+    if dtype != in_dtype and (in_dtype, dtype) != (torch.float32, torch.bfloat16):
+        raise ValueError(f"{in_dtype} gradients cannot be given back as {dtype}")
+    pos = spec.positions_tensor
+    if pos is not None and (pos.device != dev or pos.shape[-2] != N or (pos.dim() == 3 and pos.shape[0] != B)):
+        raise ValueError(f"positions {tuple(pos.shape)} on {pos.device} do not fit {B} sequences of {N} tokens on {dev}")
+    heads, outs = [], []
+    given = out if out is not None else (None, None)
+    for name, x, y in zip(names, (q, k), given):
+        if x is None:
+            heads.append(0)
+            outs.append(None)
+            continue
+        H = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 4 else 0
+        _check_heads(name, x, B, H, N, D, in_dtype, dev)
+        if y is None:
+            y = torch.empty(B, H, N, D, dtype=dtype, device=dev)
+        else:
+            _check_heads(f"out of {name}", y, B, H, N, D, dtype, dev)
+            _check_in_place(f"out of {name}", x, y)
+        heads.append(H)
+        outs.append(y)
+    code = {torch.bfloat16: 0, torch.float32: 1}
+    lib = load_library()
+    args = (_tensor(q), _tensor(outs[0]), _tensor(k), _tensor(outs[1]), _stream_handle(dev))
+    with torch.cuda.device(dev):
+        if backward:
+            st = lib.sla_rotary_backward(ctypes.byref(spec), B, *heads, N, D, code[in_dtype], code[dtype], *args)
+        else:
+            st = lib.sla_rotary(ctypes.byref(spec), B, *heads, N, D, code[in_dtype], *args)
+    _raise(st)
+    return outs[0], outs[1]
+
+
+def rotary(q, k, spec, out=None):
+    """sla_rotary: q [B,H,N,D] and k [B,Hk,N,D] (bf16 or fp32; either may be None) turned by their
+    tokens' positions.
+
+    Any strides with contiguous channels: a projection's [B,N,H,D] output goes in as its
+    transpose(1, 2). Returns contiguous tensors, or the pair `out` (an entry may be its own input:
+    in place)."""
+    return _rotary_call(q, k, spec, out, None, ("q", "k"), False)
+
+
+def rotary_backward(dq, dk, spec, dtype=None, out=None):
+    """sla_rotary_backward: the gradients of rotary's inputs from those of its outputs. dtype: of
+    the result (the gradients' own, or bf16 for fp32 gradients, as backward gives them)."""
+    return _rotary_call(dq, dk, spec, out, dtype, ("dq", "dk"), True)
+
+
+def attend_problem(q, k, causal=False, scale=None) -> AttendProblem:
+    """The sla_attend_problem of q [B,H,Nq,D] and k [B,Hk,Nk,D]."""
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, D] tensors")
+    B, H, Nq, D = q.shape
+    scale = float(scale) if scale is not None else max(D, 1) ** -0.5
+    return AttendProblem(B, H, k.shape[1], Nq, k.shape[2], D, int(bool(causal)), scale)
+
+
+def new_workspace_attend(p: AttendProblem, device, backward: bool = False) -> torch.Tensor:
+    """A zero-headed workspace for attend (backward=True: attend_backward) of problem p on device."""
+    ws = _attend_space(p, device, backward)
+    ws[:256].zero_()
+    return ws
+
+
+def _attend_space(p, device, backward):
+    lib = load_library()
+    n = (lib.sla_workspace_size_attend_backward if backward else lib.sla_workspace_size_attend)(ctypes.byref(p))
+    if n == 0:
+        raise SlaError(1, lib.sla_last_error().decode(errors="replace"))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _attend_inputs(q, k, v, kv_lens, causal, scale):
+    p = attend_problem(q, k, causal, scale)
+    dev = q.device
+    _check_heads("q", q, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    _check_heads("k", k, p.B, p.Hk, p.Nk, p.D, torch.bfloat16, dev)
+    _check_heads("v", v, p.B, p.Hk, p.Nk, p.D, torch.bfloat16, dev)
+    if kv_lens is not None and (not isinstance(kv_lens, torch.Tensor) or kv_lens.dtype != torch.int32
+                                or tuple(kv_lens.shape) != (p.B,) or not kv_lens.is_contiguous()
+                                or kv_lens.device != dev):
+        raise ValueError(f"kv_lens must be contiguous int32 [{p.B}] on {dev}")
+    return p, dev
+
+
+def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
+    """sla_attend: (out [B,H,Nq,D] bf16, lse [B,H,Nq] fp32) of softmax(scale q k^T) v.
+
+    q [B,H,Nq,D], k and v [B,Hk,Nk,D] bf16 with contiguous channels and any other strides; Hk
+    divides H. kv_lens: int32 [B] keys of each sequence (None: Nk). causal: query i sees the keys
+    j <= i + len - Nq. scale: 1 / sqrt(D) if None. A query without keys gives 0 and lse = -inf.
+    ws: new_workspace_attend's, kept where a device-side error is to be asked for with check(ws)."""
+    p, dev = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    if out is None:
+        out = torch.empty(p.B, p.H, p.Nq, p.D, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    lse = torch.empty(p.B, p.H, p.Nq, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = _attend_space(p, dev, False)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.sla_attend(ctypes.byref(p), _tensor(q), _tensor(k), _tensor(v), _ptr(kv_lens), _tensor(out), _ptr(lse),
+                            _ptr(ws), ctypes.c_size_t(ws.numel()), _stream_handle(dev))
+    _raise(st)
+    return out, lse
+
+
+def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=None, ws=None):
+    """sla_attend_backward: (dq [B,H,Nq,D], dk, dv [B,Hk,Nk,D]) bf16 of sum(dO * out), from attend's
+    out and lse of the same arguments. Equal calls give equal bits."""
+    p, dev = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    _check_heads("dO", dO, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != (p.B, p.H, p.Nq) \
+            or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError(f"lse must be contiguous fp32 [{p.B}, {p.H}, {p.Nq}] on {dev}")
+    dq = torch.empty(p.B, p.H, p.Nq, p.D, dtype=torch.bfloat16, device=dev)
+    dk, dv = (torch.empty(p.B, p.Hk, p.Nk, p.D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    if ws is None:
+        ws = _attend_space(p, dev, True)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.sla_attend_backward(ctypes.byref(p), _tensor(q), _tensor(k), _tensor(v), _tensor(out), _ptr(lse),
+                                     _tensor(dO), _ptr(kv_lens), _tensor(dq), _tensor(dk), _tensor(dv), _ptr(ws),
+                                     ctypes.c_size_t(ws.numel()), _stream_handle(dev))
+    _raise(st)
+    return dq, dk, dv
 
 
 def check(ws: torch.Tensor):

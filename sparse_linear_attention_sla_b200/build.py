@@ -2,7 +2,7 @@
 
     python -m sparse_linear_attention_sla_b200.build [--force]
 
-nvcc cross-compiles for sm_100a without a GPU. The CUDA runtime is linked
+nvcc cross-compiles for sm_100a without a GPU, one process per translation unit. The CUDA runtime is linked
 statically so the library loads in any process that has the NVIDIA driver.
 """
 
@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,10 +22,9 @@ LIB = os.path.join(PKG, "libsla.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC", "-cudart", "static",
-    "-Xptxas", "-v",
+    "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static"]
 
 
 def sources():
@@ -50,18 +50,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libsla.so if it is missing or older than its sources; return its path."""
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "sla_api.cu"), "-o", LIB + ".tmp"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
     log = os.path.join(PKG, "build.log")
+    text = ""
+    with tempfile.TemporaryDirectory() as tmp:
+        units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+        objects = [os.path.join(tmp, os.path.basename(u) + ".o") for u in units]
+        cmds = [[nvcc_path(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c", u, "-o", o]
+                for u, o in zip(units, objects)]
+        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+        results = [(p.communicate()[0], p.returncode) for p in procs]
+        if all(rc == 0 for _, rc in results):
+            cmds.append([nvcc_path(), *LINK_FLAGS, *objects, "-o", LIB + ".tmp"])
+            res = subprocess.run(cmds[-1], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            results.append((res.stdout, res.returncode))
+        for cmd, (out, _) in zip(cmds, results):
+            text += " ".join(cmd) + "\n" + out
     with open(log, "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        sys.stderr.write(res.stderr[-6000:])
-        raise RuntimeError(f"nvcc failed (exit {res.returncode}); see {log}")
+        f.write(text)
+    rc = max((rc for _, rc in results), key=abs)
+    if rc != 0:
+        sys.stderr.write(text[-6000:])
+        raise RuntimeError(f"nvcc failed (exit {rc}); see {log}")
     os.replace(LIB + ".tmp", LIB)
     if verbose:
-        print(res.stderr)
+        print(text)
     return LIB
 
 

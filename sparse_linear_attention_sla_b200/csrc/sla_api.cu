@@ -1,16 +1,9 @@
 // Host side of the C ABI declared in include/sla.h: argument checks, block
 // counts, workspace layout, TMA descriptors and kernel launches.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
-#include <mutex>
-#include <string>
 #include <utility>
 
-#include <cudaTypedefs.h>
-
-#include "../../include/sla.h"
 #include "aggregate.cuh"
 #include "attention.cuh"
 #include "attention_fp8.cuh"
@@ -18,12 +11,15 @@
 #include "backward_kv.cuh"
 #include "backward_states.cuh"
 #include "fp8.cuh"
+#include "host.cuh"
 #include "pisa.cuh"
 #include "prep.cuh"
 #include "route.cuh"
 #include "variants.cuh"
 
 namespace {
+
+using namespace sla_host;
 
 using sla::AggArgs;
 using sla::AttnArgs;
@@ -33,23 +29,6 @@ using sla::CertArgs;
 using sla::SelectArgs;
 
 constexpr int kMaxNk = 16384;
-thread_local std::string g_last_error;
-
-sla_status fail(sla_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return st;
-}
-
-#define SLA_CUDA(call)                                                                     \
-  do {                                                                                     \
-    cudaError_t e_ = (call);                                                               \
-    if (e_ != cudaSuccess) return fail(SLA_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
 
 // ------------------------------------------------------------------ shape
 
@@ -137,8 +116,6 @@ struct Workspace {
   size_t bytes;
 };
 
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
 Workspace layout(const Shape& s, uint8_t* base, bool fp8 = false, bool bwd = false, bool pisa = false) {
   Workspace w{};
   size_t off = 0;
@@ -204,43 +181,7 @@ sla_status check_ws(const Shape& s, void* ws, size_t ws_bytes, Workspace* w, boo
   return SLA_OK;
 }
 
-bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
-
 // ------------------------------------------------------------------ TMA descriptors
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// Tensor map with 128-byte swizzle (bf16, or uint8 for e4m3 codes). dims/strides in
-// elements (innermost first).
-sla_status make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides_el,
-                    const uint32_t* box, bool u8 = false) {
-  auto fn = encode_fn();
-  if (!fn) return fail(SLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], es[5];
-  for (int r = 0; r < rank; ++r) {
-    d[r] = dims[r];
-    b[r] = box[r];
-    es[r] = 1;
-  }
-  for (int r = 0; r + 1 < rank; ++r) st[r] = strides_el[r] * (u8 ? 1 : 2);
-  CUresult res = fn(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, st, b, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (res != CUDA_SUCCESS) return fail(SLA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(res));
-  return SLA_OK;
-}
 
 // [BH, N, D] activation map with a box of `rows` tokens x 64 channels.
 sla_status act_map(CUtensorMap* m, const void* ptr, const Shape& s, uint32_t rows) {
@@ -259,52 +200,6 @@ sla_status code_map(CUtensorMap* m, const void* ptr, const Shape& s, uint32_t ro
 }
 
 // ------------------------------------------------------------------ launch helpers
-
-int sm_count() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
-}
-
-template <typename K>
-sla_status allow_smem(K kernel, int bytes) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return fail(SLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-  return SLA_OK;
-}
-
-// Launch `kernel` as a programmatic dependent of the previous kernel in the stream: it may
-// be scheduled while the predecessor drains and waits (griddepcontrol.wait) before
-// reading the predecessor's results.
-template <typename... KArgs, typename... Args>
-sla_status launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                            const char* what, Args&&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-  if (e != cudaSuccess) return fail(SLA_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
-  return SLA_OK;
-}
-
-sla_status launched(const char* what) {
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(SLA_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
-  return SLA_OK;
-}
-
-#define SLA_TRY(x)                 \
-  do {                             \
-    sla_status st_ = (x);          \
-    if (st_ != SLA_OK) return st_; \
-  } while (0)
 
 template <int D>
 sla_status launch_pool(const void* x, double* out, const Shape& s, int block, int nblocks, cudaStream_t st) {
@@ -1259,6 +1154,7 @@ sla_status sla_check(void* ws, void* stream) {
   const uint32_t zero = 0;
   SLA_CUDA(cudaMemcpy(ws, &zero, sizeof(zero), cudaMemcpyHostToDevice));
   if (word & sla::SLA_DEVERR_TIMEOUT) return fail(SLA_ERR_TIMEOUT, "a device-side wait timed out (error word %u)", word);
+  if (word & sla::SLA_DEVERR_BAD_LEN) return fail(SLA_ERR_BAD_LEN, "a key length lay outside [0, Nk] (error word %u)", word);
   return fail(SLA_ERR_BAD_MASK, "caller mask held a label outside {0,1,2} (error word %u)", word);
 }
 
@@ -1272,7 +1168,7 @@ sla_status sla_selftest_wait_timeout(void* ws, size_t ws_bytes, unsigned limit_u
   return launched("wait_selftest_kernel");
 }
 
-const char* sla_last_error(void) { return g_last_error.c_str(); }
+const char* sla_last_error(void) { return sla_host::last_error(); }
 
 const char* sla_version(void) { return "sla-b200 0.1.0 (sm_100a)"; }
 
