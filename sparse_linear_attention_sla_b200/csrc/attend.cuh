@@ -13,17 +13,23 @@
 // tensor cores (each p by at most 2^-8 of itself, independently; l sums the unrounded p);
 // S, acc, m and l are fp32. A row without keys gives out = 0 and lse = -inf.
 //
-// One persistent CTA per SM, 320 threads, on units of 256 query rows of one head (two tiles A
-// and B of 128 rows) x a range of 128-key tiles:
-//   warp 0       TMA: Q tiles, then K_j and V_j through a ring of five tiles
-//   warp 1       TMEM owner and tcgen05 issuer: S_x = Q_x K_j^T, acc_x += P_x V_j. While
-//                tile A's warps turn S into P, the tensor cores run tile B's products.
-//   warps 2..5   softmax of tile A; warps 6..9 of tile B: thread = query row = TMEM lane
-// TMEM columns: S_A [0,128) S_B [128,256) (P, bf16, over the first 64 of its S), acc_A
-// [256,256+D), acc_B [384,384+D). MMAs of one thread run in issue order, so S_{j+1} never
-// overwrites P_j before the product that reads it.
-// With few units the key tiles of a unit are split over several CTAs, which write fp32 rows
-// and log2-sums that attend_join_kernel joins in a fixed order.
+// One persistent CTA per SM, 384 threads. A unit is, with more than 128 queries, 256 query rows
+// of one head (tiles A and B of 128 rows) that meet the same key tiles; with fewer ("narrow"),
+// one tile of as many (query head of the group, query) rows as fit, whose key tiles go to A and
+// B in turn, so that a single token of a group reads its keys once and both halves work:
+//   warp 0       TMA: Q, then K_j and V_j tiles through a ring
+//   warps 1, 3   tcgen05 issuers of A and of B, on blocks t of 64 keys (half a tile):
+//                S_x = Q_x K_t^T, acc_x += P_x V_t
+//   warp 2       scheduler: the CTA's units
+//   warps 4..7   softmax of A; warps 8..11 of B: thread = query row = TMEM lane
+// TMEM columns: S_A [0,128) and S_B [128,256), two buffers of 64 columns each (P_t, bf16, over the
+// first 32 of its S_t), acc_A [256,256+D), acc_B [384,384+D). MMAs of one thread run in issue
+// order, so S_{t+2} never overwrites P_t before the product that reads it; S_{t+1} is there when
+// the warps have formed P_t. (One buffer of 128 keys needs fewer tensor cycles, 2048 instead of
+// 2540 for a tile of A and of B, but then the exponentials and the products of a tile take
+// turns: 4600 cycles.)
+// Parts of units (see AttendWork) are fp32 rows divided by their own sum, with the sum's log2;
+// attend_join_kernel joins them.
 #pragma once
 
 #include "attend_common.cuh"
@@ -40,39 +46,88 @@ struct AttendSmem {
 
 struct AttendFwdArgs {
   AttendArgs p;
+  int narrow;        // Nq <= 128: units are one tile of `heads` x Nq rows
+  int heads;         // narrow: query heads of a tile, at most 128 / Nq
+  int q_bytes;       // of one loaded Q tile
   RowOut out;
   float* lse;        // [B * H, Nq]
-  float* part;       // splits > 1: [splits][B * H * Nq][D] rows, each already divided by its l
-  float* part_lse2;  // [splits][B * H * Nq] log2 of the part's sum, m included
+  float* part;       // [2 * CTAs][rows of a unit][D]
+  float* part_lse2;  // [2 * CTAs][rows of a unit]: log2 of the part's sum, its reference included
 };
 
 struct AttendUnit {
-  int b, h, row0, split;
+  int b, h, hk;  // h: the (first) query head
+  int row0;      // first query of the unit
   int len;
-  int lo, n[2];  // first key tile, key tiles of tile A and of tile B in this unit
+  int tiles[2];  // key tiles that tile A and tile B see (narrow: both, together)
+
+  __device__ __forceinline__ int steps(int narrow) const {
+    return narrow ? (tiles[0] + 1) / 2 : max(tiles[0], tiles[1]);
+  }
+  // Key tiles of x in the steps [lo, hi), and the j-th of them.
+  __device__ __forceinline__ int count(int narrow, int x, int lo, int hi) const {
+    return narrow ? max(0, min(hi, (tiles[0] - x + 1) / 2) - lo) : max(0, min(hi, tiles[x]) - lo);
+  }
 };
 
-__device__ __forceinline__ AttendUnit attend_unit(const AttendArgs& a, int u, bool record) {
+// What the warps need of the current unit.
+struct AttendItemView {
+  int b, h, hk, row0, len;
+  int lo, na, nb; // first step; key tiles of A and B
+  int slot;       // of its parts, -1: the unit is whole
+  int narrow;
+
+  __device__ __forceinline__ AttendItemView(const AttendItem& i, int nar)
+      : b(i.v[0]), h(i.v[1]), hk(i.v[2]), row0(i.v[3]), len(i.v[4]), lo(i.v[5]), na(i.v[6]), nb(i.v[7]),
+        slot(i.v[8]), narrow(nar) {}
+  __device__ __forceinline__ bool stop() const { return b < 0; }
+  __device__ __forceinline__ int n(int x) const { return x ? nb : na; }
+  __device__ __forceinline__ int tile(int x, int j) const { return narrow ? 2 * (lo + j) + x : lo + j; }
+  // Blocks of 64 keys of x: its last tile may hold no second one.
+  __device__ __forceinline__ int blocks(int x) const {
+    return n(x) == 0 ? 0 : 2 * n(x) - (len - tile(x, n(x) - 1) * kTile <= 64 ? 1 : 0);
+  }
+};
+
+__device__ __forceinline__ AttendUnit attend_unit(const AttendFwdArgs& f, int u, bool record) {
+  const AttendArgs& a = f.p;
   AttendUnit w;
+  if (f.narrow) {
+    const int groups = (a.G + f.heads - 1) / f.heads;
+    w.b = u / groups / a.Hk;
+    w.hk = u / groups % a.Hk;
+    w.h = w.hk * a.G + u % groups * f.heads;
+    w.row0 = 0;
+    w.len = attend_len(a, w.b, record);
+    w.tiles[0] = w.tiles[1] = tiles_of(attend_key_end(a, w.len, a.Nq - 1));
+    return w;
+  }
   const int pairs = (a.Nq + 2 * kTile - 1) / (2 * kTile);
-  w.split = u % a.splits;
-  const int t = u / a.splits;
-  const int pr = t % pairs, bh = t / pairs;
+  const int bh = u / pairs;
   w.b = bh / a.H;
   w.h = bh % a.H;
-  w.row0 = (a.causal ? pairs - 1 - pr : pr) * 2 * kTile;  // causal: the longest rows first
+  w.hk = w.h / a.G;
+  w.row0 = u % pairs * 2 * kTile;
   w.len = attend_len(a, w.b, record);
-  int all[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = w.row0 + x * kTile;
-    all[x] = r < a.Nq ? tiles_of(attend_key_end(a, w.len, min(r + kTile, a.Nq) - 1)) : 0;
+    w.tiles[x] = r < a.Nq ? tiles_of(attend_key_end(a, w.len, min(r + kTile, a.Nq) - 1)) : 0;
   }
-  int hi;
-  split_range(max(all[0], all[1]), a.splits, w.split, w.lo, hi);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) w.n[x] = max(0, min(hi, all[x]) - w.lo);
   return w;
+}
+
+// The head and query of row r of the unit's tile x; false where the row is none.
+template <class Unit>
+__device__ __forceinline__ bool attend_row(const AttendFwdArgs& f, const Unit& w, int x, int r, int& h, int& i) {
+  if (f.narrow) {
+    h = w.h + r / f.p.Nq;
+    i = r % f.p.Nq;
+    return r < f.heads * f.p.Nq && h < (w.hk + 1) * f.p.G;
+  }
+  h = w.h;
+  i = w.row0 + x * kTile + r;
+  return i < f.p.Nq;
 }
 
 // Keys of 32 columns from key0 on that a row does not see (its keys end at `end`) take -inf.
@@ -83,220 +138,273 @@ __device__ __forceinline__ void mask_cols32(uint32_t (&x)[32], int key0, int end
 }
 
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttendFwdArgs f) {
   using L = AttendSmem<D>;
-  constexpr int DB = D / 64, ST = L::STAGES;
+  constexpr int DB = D / 64;
   constexpr uint32_t ACC = 256;
+  // Narrow: the second Q tile's room is a stage more, and A and B have half of them each.
+  const uint32_t ST = f.narrow ? (L::STAGES + 1) / 2 : L::STAGES;
   const AttendArgs& a = f.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
-  uint8_t* ring = sQ + 2 * L::TILE;
+  uint8_t* ring = sQ + (2 - f.narrow) * L::TILE;
 
-  __shared__ uint64_t q_full[2], q_free[2], s_full[2], p_full[2], pv_done[2], acc_free[2];
-  __shared__ uint64_t full[ST], empty[ST];
+  __shared__ uint64_t q_full, q_free, s_full[2][2], p_full[2][2], pv_done[2][2], acc_free[2], b_sums;  // [x][buffer]
+  __shared__ uint64_t full[L::STAGES + 1], empty[L::STAGES + 1];
   __shared__ uint64_t drain;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ float sums[2][kTile];  // narrow: m and l of B's rows
+  __shared__ ItemRing items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int narrow = f.narrow;
   if (tid == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_free, 2);
+    mbar_init(&b_sums, 128);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 1);
-      mbar_init(&q_free[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 128);
-      mbar_init(&pv_done[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[x][b], 1);
+        mbar_init(&p_full[x][b], 128);
+        mbar_init(&pv_done[x][b], 1);
+      }
       mbar_init(&acc_free[x], 128);
     }
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s <= L::STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], narrow ? 1 : 2);  // narrow: A and B have stages of their own
     }
-    mbar_init(&drain, 1);
+    mbar_init(&drain, 2);
+    items.init();
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(&tmem_base_sh, 512);
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base_sh, 512);  // all columns, so column addresses count from 0
     tmem_relinquish();
   }
+  grid_dep_wait();  // lengths and inputs may come from earlier kernels
+  const auto steps = [&](int u) { return attend_unit(f, u, false).steps(narrow); };
+  AttendWork work = attend_work(a, steps, kThreads);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
-  grid_dep_wait();
+  AttendItem item;
 
-  if (warp == 0) {
+  if (warp < 4) regs_down<kIssueRegs>();
+  if (warp == kScheduleWarp) {
+    if (lane == 0) {
+      uint32_t ni = 0;
+      int u, lo, hi, n, to;
+      bool ok = true;
+      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+        note_part(a, work, u, lo, hi, n, to);
+        const AttendUnit w = attend_unit(f, u, true);
+        item = {w.b, w.h, w.hk, w.row0, w.len, lo, w.count(narrow, 0, lo, hi), w.count(narrow, 1, lo, hi),
+                part_slot(lo, hi, n)};
+        ok = items.put(ni++, item, a.err, &abort_flag);
+      }
+      item.v[0] = -1;
+      if (ok) items.put(ni, item, a.err, &abort_flag);
+    }
+    __syncwarp();
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       prefetch_tmap(&map_q);
       prefetch_tmap(&map_k);
       prefetch_tmap(&map_v);
-      uint32_t nr = 0, nq[2] = {0, 0};  // ring tiles and Q tiles loaded
+      RingPos pos[2];  // wide: only the first
+      uint32_t nr[2] = {0, 0}, nq = 0, ni = 0;  // ring tiles, Q loads and items so far
       bool ok = true;
-      auto load_q = [&](const AttendUnit& w, int x) {
-        if (w.n[x] == 0) return;
-        if (nq[x] > 0 && !(ok = mbar_wait(&q_free[x], (nq[x] - 1) & 1, a.err, &abort_flag))) return;
-        mbar_arrive_expect_tx(&q_full[x], L::TILE);
-        for (int b = 0; b < DB; ++b)
-          tma_load_4d(sQ + x * L::TILE + b * kBox, &map_q, &q_full[x], b * 64, w.row0 + x * kTile, w.h, w.b);
-        ++nq[x];
-      };
-      auto load = [&](const CUtensorMap* m, const AttendUnit& w, int j) {
-        const uint32_t s = nr % ST, r = nr / ST;
-        if (r > 0 && !(ok = mbar_wait(&empty[s], (r - 1) & 1, a.err, &abort_flag))) return;
-        mbar_arrive_expect_tx(&full[s], L::TILE);
-        for (int b = 0; b < DB; ++b)
-          tma_load_4d(ring + s * L::TILE + b * kBox, m, &full[s], b * 64, j * kTile, w.h / a.G, w.b);
-        ++nr;
-      };
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-        const AttendUnit w = attend_unit(a, u, true);
-        const int n = max(w.n[0], w.n[1]);
-        if (n == 0) continue;
-        load_q(w, 0);
-        if (ok) load(&map_k, w, w.lo);
-        if (ok) load_q(w, 1);
-        for (int j = 0; ok && j < n; ++j) {
-          load(&map_v, w, w.lo + j);
-          if (ok && j + 1 < n) load(&map_k, w, w.lo + j + 1);
+      while (ok) {
+        if (!(ok = items.get_one(ni++, item, a.err, &abort_flag))) break;
+        const AttendItemView w(item, narrow);
+        if (w.stop()) break;
+        if (w.n(0) + w.n(1) == 0) continue;
+        auto load = [&](const CUtensorMap* m, int x, int j) {
+          const uint32_t s = x * ST + pos[x].s;
+          if (nr[x] >= ST && !(ok = mbar_wait(&empty[s], pos[x].parity ^ 1, a.err, &abort_flag))) return;
+          mbar_arrive_expect_tx(&full[s], L::TILE);
+          for (int b = 0; b < DB; ++b)
+            tma_load_4d(ring + s * L::TILE + b * kBox, m, &full[s], b * 64, w.tile(x, j) * kTile, w.hk, w.b);
+          ++nr[x];
+          pos[x].next(ST);
+        };
+        if (nq > 0) ok = mbar_wait(&q_free, (nq - 1) & 1, a.err, &abort_flag);
+        if (ok) {
+          const int q_tiles = narrow || w.n(1) == 0 ? 1 : 2;
+          mbar_arrive_expect_tx(&q_full, q_tiles * f.q_bytes);
+          for (int x = 0; x < q_tiles; ++x)
+            for (int b = 0; b < DB; ++b)
+              tma_load_5d(sQ + x * L::TILE + b * kBox, &map_q, &q_full, b * 64, w.row0 + x * kTile, w.h % a.G, w.hk,
+                          w.b);
+          ++nq;
+        }
+        if (narrow) {
+          for (int x = 0; ok && x < 2; ++x)
+            if (w.n(x) > 0) load(&map_k, x, 0);
+          for (int j = 0; ok && j < w.n(0); ++j) {
+            for (int x = 0; ok && x < 2; ++x) {
+              if (j >= w.n(x)) continue;
+              load(&map_v, x, j);
+              if (ok && j + 1 < w.n(x)) load(&map_k, x, j + 1);
+            }
+          }
+        } else {
+          const int nt = max(w.n(0), w.n(1));
+          if (ok) load(&map_k, 0, 0);
+          for (int j = 0; ok && j < nt; ++j) {
+            load(&map_v, 0, j);
+            if (ok && j + 1 < nt) load(&map_k, 0, j + 1);
+          }
         }
       }
       if (abort_flag) {  // let every load still in flight land before the CTA retires
+        if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1, nullptr, nullptr);
         for (int x = 0; x < 2; ++x)
-          if (nq[x] > 0) mbar_wait(&q_full[x], (nq[x] - 1) & 1, nullptr, nullptr);
-        for (uint32_t i = nr > ST ? nr - ST : 0; i < nr; ++i)
-          mbar_wait(&full[i % ST], (i / ST) & 1, nullptr, nullptr);
+          for (uint32_t i = nr[x] > ST ? nr[x] - ST : 0; i < nr[x]; ++i)
+            mbar_wait(&full[x * ST + i % ST], (i / ST) & 1, nullptr, nullptr);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t q0 = smem_u32(sQ), r0 = smem_u32(ring);
-    uint32_t nr = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // ring tiles, units and P tiles consumed
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
+    // ------------------------------------------------------------ MMA issuer of tile x
+    const int x = warp == kMmaWarp2;
+    const uint32_t q0 = smem_u32(sQ) + (narrow ? 0 : x * L::TILE), r0 = smem_u32(ring);
+    const uint32_t first = narrow ? x * ST : 0;  // this warp's first stage
+    RingPos pos;
+    uint32_t nq = 0, ni = 0, nu = 0, g = 0;  // units with work, items, units with tiles of x, blocks before the unit
     bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
-    };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const AttendUnit w = attend_unit(a, u, false);
-      const int n = max(w.n[0], w.n[1]);
-      if (n == 0) continue;
-      // S of key tile j (0-based in the unit) from ring stage sk, for query tile x.
-      auto issue_s = [&](int x, int j, uint32_t sk) {
-        if (elect_one()) {
-          issue_ss<D>(tmem + x * 128, q0 + x * L::TILE, r0 + sk * L::TILE);
-          umma_commit(&s_full[x]);
-          if (j + 1 == w.n[x]) umma_commit(&q_free[x]);
-        }
-        __syncwarp();
-      };
-      uint32_t sk = nr % ST;
-      if (!(ok = wait_all(&full[sk], (nr / ST) & 1))) break;
-      ++nr;
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (w.n[x] == 0) continue;
-        if (!(ok = wait_all(&q_full[x], nu[x] & 1))) break;
-        tc_fence_after();
-        issue_s(x, 0, sk);
-      }
-      if (!ok) break;
-      if (elect_one()) umma_commit(&empty[sk]);
+    const uint32_t lead = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
+    auto commit = [&](uint64_t* bar) { mma_commit(lead, bar); };
+    auto arrive = [&](uint64_t* bar) {
+      if (lane == 0) mbar_arrive(bar);
       __syncwarp();
-      for (int j = 0; ok && j < n; ++j) {
-        const uint32_t sv = nr % ST;
-        if (!(ok = wait_all(&full[sv], (nr / ST) & 1))) break;
-        ++nr;
-        const int keys = w.len - (w.lo + j) * kTile;  // real keys of the tile
-        if (keys < kTile) zero_rows<D>(ring + sv * L::TILE, keys, kTile);
-        const bool more = j + 1 < n;
-        if (more) {
-          sk = nr % ST;
-          if (!(ok = wait_all(&full[sk], (nr / ST) & 1))) break;
-          ++nr;
-        }
-        for (int x = 0; x < 2; ++x) {
-          if (j >= w.n[x]) continue;
-          if (j == 0 && nu[x] > 0 && !(ok = wait_all(&acc_free[x], (nu[x] - 1) & 1))) break;
-          if (!(ok = wait_all(&p_full[x], np[x] & 1))) break;
-          ++np[x];
-          tc_fence_after();
-          if (elect_one()) {
-            issue_ts<D, 32>(tmem + ACC + x * 128, tmem + x * 128, r0 + sv * L::TILE, j > 0);
-            umma_commit(&pv_done[x]);
-          }
-          __syncwarp();
-          if (j + 1 < w.n[x]) issue_s(x, j + 1, sk);
-        }
-        if (!ok) break;
-        if (elect_one()) {
-          umma_commit(&empty[sv]);
-          if (more) umma_commit(&empty[sk]);
-        }
-        __syncwarp();
+    };
+    // The next ring tile, once it has landed.
+    auto take = [&](uint32_t& s) -> bool {
+      s = first + pos.s;
+      const bool r = wait(&full[s], pos.parity);
+      pos.next(ST);
+      return r;
+    };
+    // S of block t of the unit, from its half of the K tile in stage sk.
+    auto issue_s = [&](int t, uint32_t sk) {
+      const uint32_t b = (g + t) & 1;
+      issue_ss<D, 64>(lead, x * 128 + b * 64, q0, r0 + sk * L::TILE + (t & 1) * 8192);
+      commit(&s_full[x][b]);
+    };
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const AttendItemView w(item, narrow);
+      if (w.stop()) break;
+      const int n = w.n(x), loaded = narrow ? n : max(w.na, w.nb);  // tiles of x; tiles that the ring brings
+      const int nb = w.blocks(x);
+      if (max(w.na, w.nb) == 0) continue;
+      uint32_t sk = 0, sv = 0;  // stages of the current K and V tile
+      if (!(ok = wait(&q_full, nq & 1))) break;
+      ++nq;
+      if (n > 0) {
+        if (!(ok = take(sk))) break;
+        tc_fence_after();
+        issue_s(0, sk);
+        if (nb > 1) issue_s(1, sk);
+        commit(&empty[sk]);
       }
-      for (int x = 0; x < 2; ++x) nu[x] += w.n[x] > 0;
+      if (n == 1) commit(&q_free);
+      if (n == 0) arrive(&q_free);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = take(sv))) break;
+        const int keys = w.len - w.tile(x, j) * kTile;  // rows behind the sequence's keys
+        if (keys < kTile) zero_rows<D>(ring + sv * L::TILE, keys, kTile);
+        if (j == 0 && nu > 0 && !(ok = wait(&acc_free[x], (nu - 1) & 1))) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 2 * j + e;
+          if (t >= nb) break;
+          const uint32_t b = (g + t) & 1;
+          if (!(ok = wait(&p_full[x][b], ((g + t) >> 1) & 1))) break;
+          tc_fence_after();
+          issue_ts<D, 0, 4, 32>(lead, ACC + x * 128, x * 128 + b * 64, r0 + sv * L::TILE + e * 8192, t > 0);
+          commit(&pv_done[x][b]);
+          if (e == 1 || t + 1 == nb) commit(&empty[sv]);
+          if (j + 1 < n) {
+            if (e == 0 && !(ok = take(sk))) break;
+            tc_fence_after();
+            if (t + 2 < nb) issue_s(t + 2, sk);
+            if (e == 1) commit(&empty[sk]);
+          }
+        }
+        if (j + 2 == n) commit(&q_free);  // no S of this unit is left to issue
+      }
+      // Wide: tiles that only the other query tile needs.
+      for (int j = 2 * n; ok && j < 2 * loaded; ++j) {
+        if (!(ok = take(sk))) break;
+        arrive(&empty[sk]);
+      }
+      nu += n > 0;
+      g += nb;
     }
-    if (elect_one()) umma_commit(&drain);  // every MMA issued above has finished once this arrives
-    __syncwarp();
+    commit(&drain);  // every MMA issued above has finished once this arrives
     mbar_wait(&drain, 0, nullptr, nullptr);
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax warpgroups
-    const int x = warp >= 6;
+    regs_up<kComputeRegs>();
+    const int x = warp >= 8;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = lane_addr + x * 128, o_addr = lane_addr + ACC + x * 128;
     const float sc = a.scale_log2;
     const uint64_t sc2 = f2_make(sc, sc);
-    uint32_t ns = 0;  // S tiles so far
+    uint32_t ni = 0, ns = 0, nu = 0, nbb = 0;  // items; blocks of x; narrow: units with tiles of B, and their blocks
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
-    };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const AttendUnit w = attend_unit(a, u, false);
-      const int row = w.row0 + x * kTile + r;
-      const int n = w.n[x];
-      const int end = attend_key_end(a, w.len, row);                          // this row's keys
-      const int end_min = attend_key_end(a, w.len, w.row0 + x * kTile);       // of the tile's first row
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const AttendItemView w(item, narrow);
+      if (w.stop()) break;
+      int h, i;
+      const bool real = attend_row(f, w, x, r, h, i);
+      const int n = w.blocks(x), other = w.blocks(x ^ 1);
+      const int end = attend_key_end(a, w.len, i);                                    // this row's keys
+      const int end_min = attend_key_end(a, w.len, narrow ? 0 : w.row0 + x * kTile);  // fewest of a row
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++ns) {
-        if (!(ok = wait(&s_full[x], ns & 1))) break;
+      for (int t = 0; t < n; ++t, ++ns) {
+        const uint32_t b = ns & 1, sb = s_addr + b * 64;
+        if (!(ok = wait(&s_full[x][b], (ns >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, s[c]);
+        uint32_t s[2][32];
+        tmem_ld32(sb, s[0]);
+        tmem_ld32(sb + 32, s[1]);
         tmem_wait_ld();
-        const int key0 = (w.lo + j) * kTile;
-        if (key0 + kTile > end_min) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mask_cols32(s[c], key0 + 32 * c, end);
+        const int key0 = w.tile(x, t >> 1) * kTile + (t & 1) * 64;
+        if (key0 + 64 > end_min) {
+          mask_cols32(s[0], key0, end);
+          mask_cols32(s[1], key0 + 32, end);
         }
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float t = fmaxf(row_max64(s[0], s[1]), row_max64(s[2], s[3])) * sc;
-          if (m == -INFINITY) m = t;
+          const float top = row_max64(s[0], s[1]) * sc;
+          if (m == -INFINITY) m = top;
         }
-        float sum;
-        auto exponentials = [&]() {
+        uint32_t pk[32];
+        auto exponentials = [&]() -> float {
           const float ref = m == -INFINITY ? 0.f : m;  // no key seen yet: every s is -inf
-          const uint64_t nm2 = f2_make(-ref, -ref);
-          uint64_t part = 0ull;
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t pk[32];
-            part = f2_add(part, exp2_block(s[c], s[c + 1], pk, sc2, nm2));
-            tmem_st32(s_addr + 16 * c, pk);
-          }
-          sum = f2_lo(part) + f2_hi(part);
+          const uint64_t part = exp2_block(s[0], s[1], pk, sc2, f2_make(-ref, -ref));
+          return f2_lo(part) + f2_hi(part);
         };
-        exponentials();
+        float sum = exponentials();
         if (__any_sync(0xffffffffu, sum > kRefMoveSum)) {
-          const float t = fmaxf(m, fmaxf(row_max64(s[0], s[1]), row_max64(s[2], s[3])) * sc);
-          const float g = m == -INFINITY ? 1.f : fast_exp2(m - t);
-          if (j > 0) {
-            if (!(ok = wait(&pv_done[x], (ns - 1) & 1))) break;
+          // Only the rows that passed move: a row's bits depend on nothing but its own scores (rows of
+          // the tile that are no query hold whatever shared memory held).
+          const float top = sum > kRefMoveSum ? fmaxf(m, row_max64(s[0], s[1]) * sc) : m;
+          const float g = m == -INFINITY ? 1.f : fast_exp2(m - top);
+          if (t > 0) {  // S_t was seen, so of the products only the last can be open
+            if (!(ok = wait(&pv_done[x][b ^ 1], ((ns - 1) >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
@@ -308,102 +416,146 @@ __global__ void __launch_bounds__(320, 1)
               tmem_st16(o_addr + c0, o);
             }
           }
-          tmem_wait_st();
           l *= g;
-          m = t;
-          exponentials();
+          m = top;
+          sum = exponentials();
         }
         l += sum;
+        tmem_st32(sb, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[x][b]);
       }
       if (!ok) break;
-      // acc / l as bf16, or as a part's fp32 row with its log2-sum
-      if (n > 0) {
-        if (!(ok = wait(&pv_done[x], (ns - 1) & 1))) break;
-        tc_fence_after();
+      // acc / l as bf16, or as a part's fp32 row with its log2-sum. Narrow: A's warps write
+      // both, w_x = 2^(m_x - m) being the weight of x's accumulator.
+      float weight[2] = {1.f, 0.f};
+      if (narrow && x == 1) {
+        if (n > 0) {
+          if (nu > 0 && !(ok = wait(&acc_free[1], (nu - 1) & 1))) break;  // the last sums have been read
+          sums[0][r] = m;
+          sums[1][r] = l;
+          mbar_arrive(&b_sums);
+          ++nu;
+        }
+        continue;
       }
-      const bool real = row < a.Nq;
+      const bool both = narrow && other > 0;
+      if (both) {
+        if (!(ok = wait(&b_sums, nu & 1) && wait(&pv_done[1][(nbb + other - 1) & 1], ((nbb + other - 1) >> 1) & 1))) break;
+        const float mb = sums[0][r], lb = sums[1][r];
+        const float top = fmaxf(m, mb);
+        weight[0] = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        weight[1] = mb == -INFINITY ? 0.f : fast_exp2(mb - top);
+        l = l * weight[0] + lb * weight[1];
+        m = top;
+        nbb += other;
+        ++nu;
+      }
+      if (n > 0 && !(ok = wait(&pv_done[x][(ns - 1) & 1], ((ns - 1) >> 1) & 1))) break;
+      tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
-      const size_t at = (static_cast<size_t>(w.b) * a.H + w.h) * a.Nq + row;
-      const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
+      const size_t part_row = narrow ? static_cast<size_t>(w.slot) * kTile + r
+                                     : static_cast<size_t>(w.slot) * 2 * kTile + x * kTile + r;
+      __nv_bfloat16* const out = f.out.p + w.b * f.out.sb + h * f.out.sh + i * f.out.sn;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t o[32];
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t o[2][32];
         if (n > 0) {
-          tmem_ld32(o_addr + c0, o);
+          tmem_ld32(o_addr + c0, o[0]);
+          tmem_ld32(o_addr + c0 + 32, o[1]);
           tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
-        if (l == 0.f) {  // nothing was seen: acc holds no number to keep
+        if (both) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0u;
+          for (int g = 0; g < 2; ++g) {
+            uint32_t ob[32];
+            tmem_ld32(o_addr + 128 + c0 + 32 * g, ob);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              o[g][c] = __float_as_uint(weight[0] * __uint_as_float(o[g][c]) + weight[1] * __uint_as_float(ob[c]));
+          }
+        }
+        if (l == 0.f) {  // nothing was seen: the accumulators hold no number to keep
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[0][c] = o[1][c] = 0u;
         }
         if (real) {
-          if (a.splits == 1)
-            store_row32(f.out.p + w.b * f.out.sb + w.h * f.out.sh + row * f.out.sn + c0, o, inv, f.out.wide);
-          else
-            store_row32(f.part + (w.split * rows + at) * D + c0, o, inv, true);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (w.slot < 0)
+              store_row32(out + c0 + 32 * g, o[g], inv, f.out.wide);
+            else
+              store_row32(f.part + part_row * D + c0 + 32 * g, o[g], inv, true);
+          }
         }
         __syncwarp();
       }
       if (real) {
-        if (a.splits == 1)
-          f.lse[at] = lse2 * 0.69314718055994531f;
+        if (w.slot < 0)
+          f.lse[(static_cast<size_t>(w.b) * a.H + h) * a.Nq + i] = lse2 * 0.69314718055994531f;
         else
-          f.part_lse2[w.split * rows + at] = lse2;
+          f.part_lse2[part_row] = lse2;
       }
-      if (n > 0) {
-        tc_fence_before();
-        mbar_arrive(&acc_free[x]);
-      }
+      tc_fence_before();
+      if (n > 0) mbar_arrive(&acc_free[x]);
+      if (both) mbar_arrive(&acc_free[1]);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem_base_sh, 512);
   }
 }
 
-// out = sum_s 2^(lse2_s - lse2) part_s in ascending s, one warp per row.
+// Joins the parts of the unit that CTA blockIdx.x of attend_kernel began and others went on
+// with: out = sum_p 2^(lse2_p - lse2) part_p in ascending CTA order, one warp per row.
 template <int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(AttendFwdArgs f) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendFwdArgs f) {
   const AttendArgs& a = f.p;
-  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
-  const size_t at = static_cast<size_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
   grid_dep_wait();
-  if (at >= rows) return;
+  const int C = gridDim.x, c0 = blockIdx.x;
+  const int4 meta = a.meta[c0];
+  if (meta.x < 0) return;
+  const int rows = f.narrow ? kTile : 2 * kTile;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const AttendUnit w = attend_unit(f, meta.x, false);
+  int h, i;
+  if (!attend_row(f, w, row / kTile, row % kTile, h, i)) return;
+  constexpr int E = D / 32;
+  // Slots: 2 c0 + 1, then 2 c of every later CTA up to meta.y.
+  auto slot_row = [&](int c) { return static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * rows + row; };
   float m = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, f.part_lse2[s * rows + at]);
+  for (int c = c0 + lane; c <= meta.y; c += 32)
+    if (!part_is_empty(meta.z, C, c)) m = fmaxf(m, f.part_lse2[slot_row(c)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
   float sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = exp2f(f.part_lse2[s * rows + at] - ref);
-    sum += w;
-    const float* p = f.part + (s * rows + at) * D + lane * E;
+#pragma unroll 4
+  for (int c = c0; c <= meta.y; ++c) {
+    if (part_is_empty(meta.z, C, c)) continue;
+    const size_t at = slot_row(c);
+    const float g = exp2f(f.part_lse2[at] - ref);
+    sum += g;
+    const float* p = f.part + at * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, p[e], acc[e]);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(g, p[e], acc[e]);
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int row = static_cast<int>(at % a.Nq);
-  const size_t bh = at / a.Nq;
-  __nv_bfloat16* out = f.out.p + (bh / a.H) * f.out.sb + (bh % a.H) * f.out.sh + row * f.out.sn + lane * E;
+  __nv_bfloat16* out = f.out.p + w.b * f.out.sb + h * f.out.sh + i * f.out.sn + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(out + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) f.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0)
+    f.lse[(static_cast<size_t>(w.b) * a.H + h) * a.Nq + i] =
+        sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace sla

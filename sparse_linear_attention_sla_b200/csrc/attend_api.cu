@@ -18,34 +18,53 @@ using sla::AttendSumArgs;
 using sla::kTile;
 using sla::RowOut;
 
-// SMs that a launch should fill: the split of the work, and so the workspace's size, must not
-// depend on which device is current.
+// CTAs that a launch has at most: the workspace's size must not depend on which device is
+// current, so a B200's 148 SMs are taken as given.
 constexpr int kSms = 148;
+
+// How one kernel's units are shared out over its CTAs (see AttendWork).
+struct Share {
+  int units, ctas, waves, uniform;
+  bool cut;  // units may be cut into parts
+};
+
+// `units` units of at most `steps` steps each. Where whole units would leave CTAs idle (fewer
+// units than CTAs, a last wave that is mostly empty, or units of unlike length), the steps
+// behind the whole waves are cut into equal ranges, at least two steps to a range.
+// Units of like length: all waves but the last two go out whole. Many units of unlike length: over 64 to a
+// CTA their differences even out, and a scan over them would cost more than it saves.
+Share share_out(long long units, long long steps, bool uniform) {
+  Share s{static_cast<int>(units), 0, 0, uniform ? 1 : 0, false};
+  const long long waves = (units + kSms - 1) / kSms;
+  const bool even = uniform && units * 100 >= waves * kSms * 95;
+  if (even || units > 64ll * kSms || units * (steps + sla::kUnitCost) >= (1ll << 31)) {
+    s.ctas = static_cast<int>(units < kSms ? units : kSms);
+    s.waves = static_cast<int>(waves);
+    return s;
+  }
+  s.waves = uniform && waves > 2 ? static_cast<int>(waves) - 2 : 0;
+  const long long ranges = (units * steps + 1) / 2;
+  s.ctas = static_cast<int>(ranges < kSms ? (ranges < 1 ? 1 : ranges) : kSms);
+  s.cut = true;
+  return s;
+}
 
 struct AttendPlan {
   sla_attend_problem p;
-  int pad;                                      // Nq rounded up to whole tiles
-  long long q_rows, k_rows;                     // B H Nq, B Hk Nk
-  int fwd_units, dkv_units, dq_units;           // with their splits
-  int fwd_splits, dkv_splits, dq_splits;
+  int pad;             // Nq rounded up to whole tiles
+  int narrow, heads;   // forward: see AttendFwdArgs
+  Share fwd, dkv, dq;
 };
 
 struct AttendSpace {
   uint32_t* err;
-  float *part, *part_lse2;              // forward
-  float *nlse, *ndelta, *dq, *dkv;      // backward
+  int4 *meta, *meta_q;              // forward or dK / dV, dQ
+  float *part, *part_lse2;          // forward, or dK / dV
+  float *nlse, *ndelta, *part_q;    // backward
   size_t bytes;
 };
 
-// Work items of a launch of `units` independent units with `tiles` steps each: fewer units
-// than SMs are split over the steps, at least two of them to a part.
-int splits_for(long long units, long long tiles) {
-  if (units >= kSms) return 1;
-  const long long by_sms = kSms / units, by_work = (tiles + 1) / 2;
-  return static_cast<int>(by_sms < by_work ? by_sms : by_work < 1 ? 1 : by_work);
-}
-
-sla_status make_plan(const sla_attend_problem* p, AttendPlan* w) {
+sla_status make_plan(const sla_attend_problem* p, bool has_lens, AttendPlan* w) {
   if (!p) return fail(SLA_ERR_INVALID_ARG, "problem is NULL");
   if (p->B < 1 || p->H < 1 || p->Hk < 1 || p->Nq < 1 || p->Nk < 1)
     return fail(SLA_ERR_INVALID_ARG, "B, H, Hk, Nq and Nk must be >= 1");
@@ -61,38 +80,47 @@ sla_status make_plan(const sla_attend_problem* p, AttendPlan* w) {
   if (group * qt >= (1ll << 30)) return fail(SLA_ERR_UNSUPPORTED, "H / Hk * Nq too large");
   w->p = *p;
   w->pad = static_cast<int>(qt * kTile);
-  w->q_rows = BH * p->Nq;
-  w->k_rows = BHk * p->Nk;
-  w->fwd_splits = splits_for(BH * pairs, kt);
-  w->dkv_splits = splits_for(BHk * kt, group * qt);
-  w->dq_splits = splits_for(BH * qt, kt);
-  w->fwd_units = static_cast<int>(BH * pairs) * w->fwd_splits;
-  w->dkv_units = static_cast<int>(BHk * kt) * w->dkv_splits;
-  w->dq_units = static_cast<int>(BH * qt) * w->dq_splits;
+  const bool uniform = !p->causal && !has_lens;
+  w->narrow = p->Nq <= kTile;
+  w->heads = 1;
+  if (w->narrow) {
+    w->heads = static_cast<int>(group < kTile / p->Nq ? group : kTile / p->Nq);
+    // one query tile sees the same keys whatever the mask
+    w->fwd = share_out(BHk * ((group + w->heads - 1) / w->heads), (kt + 1) / 2, !has_lens);
+  } else {
+    w->fwd = share_out(BH * pairs, kt, uniform);
+  }
+  w->dkv = share_out(BHk * kt, group * qt, uniform);
+  w->dq = share_out(BH * qt, kt, uniform);
   return SLA_OK;
 }
 
 AttendSpace layout(const AttendPlan& w, uint8_t* base, bool bwd) {
   AttendSpace s{};
   size_t off = 0;
-  auto take = [&](size_t floats) {
+  auto take = [&](size_t words) {
     float* p = base ? reinterpret_cast<float*>(base + off) : nullptr;
-    off += align256(floats * sizeof(float));
+    off += align256(words * sizeof(float));
     return p;
   };
+  auto meta = [&](const Share& h) { return h.cut ? reinterpret_cast<int4*>(take(4 * static_cast<size_t>(h.ctas))) : nullptr; };
   s.err = reinterpret_cast<uint32_t*>(take(64));
-  const size_t D = w.p.D;
+  const size_t row = w.p.D;
   if (!bwd) {
-    if (w.fwd_splits > 1) {
-      s.part = take(w.fwd_splits * static_cast<size_t>(w.q_rows) * D);
-      s.part_lse2 = take(w.fwd_splits * static_cast<size_t>(w.q_rows));
+    s.meta = meta(w.fwd);
+    const size_t rows = 2 * static_cast<size_t>(w.fwd.ctas) * (w.narrow ? 1 : 2) * kTile;
+    if (w.fwd.cut) {
+      s.part = take(rows * row);
+      s.part_lse2 = take(rows);
     }
   } else {
     const size_t stats = static_cast<size_t>(w.p.B) * w.p.H * w.pad;
     s.nlse = take(stats);
     s.ndelta = take(stats);
-    if (w.dq_splits > 1) s.dq = take(w.dq_splits * static_cast<size_t>(w.q_rows) * D);
-    if (w.dkv_splits > 1) s.dkv = take(2 * w.dkv_splits * static_cast<size_t>(w.k_rows) * D);
+    s.meta = meta(w.dkv);
+    s.meta_q = meta(w.dq);
+    if (w.dkv.cut) s.part = take(2 * static_cast<size_t>(w.dkv.ctas) * 2 * kTile * row);
+    if (w.dq.cut) s.part_q = take(2 * static_cast<size_t>(w.dq.ctas) * kTile * row);
   }
   s.bytes = off;
   return s;
@@ -107,6 +135,14 @@ sla_status check_space(const AttendPlan& w, void* ws, size_t ws_bytes, bool bwd,
   return SLA_OK;
 }
 
+// The workspace holds a call with key lengths as well as one without.
+size_t space_bytes(const sla_attend_problem* p, bool bwd) {
+  AttendPlan a, b;
+  if (make_plan(p, false, &a) != SLA_OK || make_plan(p, true, &b) != SLA_OK) return 0;
+  const size_t x = layout(a, nullptr, bwd).bytes, y = layout(b, nullptr, bwd).bytes;
+  return x > y ? x : y;
+}
+
 // A [B, heads, N, D] bf16 operand: rows of 16 bytes, ascending strides where the extent is
 // above 1 (a tensor map has no stride of zero).
 sla_status check_operand(const char* name, const sla_tensor* t, int B, int heads, int N) {
@@ -119,9 +155,23 @@ sla_status check_operand(const char* name, const sla_tensor* t, int B, int heads
     if (d.extent <= 1) continue;
     if (d.stride < 1 || d.stride % 8)
       return fail(SLA_ERR_INVALID_ARG, "%s's strides must be positive multiples of 16 bytes", name);
-    if (d.stride >= (1ll << 38)) return fail(SLA_ERR_UNSUPPORTED, "%s's strides must be below 2^38 elements", name);
+    if (d.stride >= (1ll << 38) / heads) return fail(SLA_ERR_UNSUPPORTED, "%s's strides are too large", name);
   }
   return SLA_OK;
+}
+
+// The queries as (channel, token, head of the group, key head, sequence): boxes of `tokens` rows of
+// `heads` heads.
+sla_status query_map(CUtensorMap* m, const sla_tensor* t, const sla_attend_problem& p, int tokens, int heads) {
+  const int G = p.H / p.Hk;
+  const uint64_t dims[5] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(p.Nq), static_cast<uint64_t>(G),
+                            static_cast<uint64_t>(p.Hk), static_cast<uint64_t>(p.B)};
+  const uint64_t strides[4] = {static_cast<uint64_t>(p.Nq > 1 ? t->stride_n : p.D),
+                               static_cast<uint64_t>(G > 1 ? t->stride_h : p.D),
+                               static_cast<uint64_t>(p.Hk > 1 ? G * t->stride_h : p.D),
+                               static_cast<uint64_t>(p.B > 1 ? t->stride_b : p.D)};
+  const uint32_t box[5] = {64, static_cast<uint32_t>(tokens), static_cast<uint32_t>(heads), 1, 1};
+  return make_map(m, t->ptr, 5, dims, strides, box);
 }
 
 // Tiles of 128 rows x 64 channels of a checked operand.
@@ -142,7 +192,7 @@ RowOut row_out(const sla_tensor* t, int B, int heads, int N) {
   return o;
 }
 
-AttendArgs common_args(const AttendPlan& w, const int32_t* lens, uint32_t* err, int splits, int units) {
+AttendArgs common_args(const AttendPlan& w, const int32_t* lens, uint32_t* err, const Share& h, int4* meta) {
   AttendArgs a{};
   a.B = w.p.B;
   a.H = w.p.H;
@@ -151,8 +201,10 @@ AttendArgs common_args(const AttendPlan& w, const int32_t* lens, uint32_t* err, 
   a.Nq = w.p.Nq;
   a.Nk = w.p.Nk;
   a.causal = w.p.causal;
-  a.splits = splits;
-  a.units = units;
+  a.units = h.units;
+  a.waves = h.waves;
+  a.uniform = h.uniform;
+  a.meta = meta;
   a.scale = w.p.scale;
   a.scale_log2 = w.p.scale * 1.4426950408889634f;
   a.lens = lens;
@@ -160,67 +212,42 @@ AttendArgs common_args(const AttendPlan& w, const int32_t* lens, uint32_t* err, 
   return a;
 }
 
-int persistent_grid(int units) {
-  const int n = sm_count();
-  return units < n ? units : n;
-}
-
 struct Maps {
   CUtensorMap q, k, v, g;
 };
-
-sla_status input_maps(Maps* m, const AttendPlan& w, const sla_tensor* q, const sla_tensor* k, const sla_tensor* v,
-                      const sla_tensor* g) {
-  SLA_TRY(operand_map(&m->q, q, w.p.B, w.p.H, w.p.Nq, w.p.D));
-  SLA_TRY(operand_map(&m->k, k, w.p.B, w.p.Hk, w.p.Nk, w.p.D));
-  SLA_TRY(operand_map(&m->v, v, w.p.B, w.p.Hk, w.p.Nk, w.p.D));
-  if (g) SLA_TRY(operand_map(&m->g, g, w.p.B, w.p.H, w.p.Nq, w.p.D));
-  return SLA_OK;
-}
 
 template <int D>
 sla_status launch_forward(const AttendPlan& w, const Maps& m, const AttendFwdArgs& f, cudaStream_t st) {
   constexpr int smem = sla::AttendSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_kernel<D>, smem));
-  SLA_TRY(launch_dependent(sla::attend_kernel<D>, dim3(persistent_grid(w.fwd_units)), dim3(320), smem, st,
-                           "attend_kernel", m.q, m.k, m.v, f));
-  if (w.fwd_splits > 1)
-    SLA_TRY(launch_dependent(sla::attend_join_kernel<D>, dim3(static_cast<unsigned>((w.q_rows + 7) / 8)), dim3(256), 0,
+  SLA_TRY(launch_dependent(sla::attend_kernel<D>, dim3(w.fwd.ctas), dim3(sla::kThreads), smem, st, "attend_kernel", m.q, m.k,
+                           m.v, f));
+  if (w.fwd.cut)
+    SLA_TRY(launch_dependent(sla::attend_join_kernel<D>, dim3(w.fwd.ctas, (w.narrow ? 1 : 2) * kTile / 8), dim3(256), 0,
                              st, "attend_join_kernel", f));
   return SLA_OK;
 }
 
 template <int D>
-sla_status launch_sum(const float* part, int splits, int H, int N, long long rows, const RowOut& out, cudaStream_t st) {
-  const AttendSumArgs a{part, splits, H, N, rows, out};
-  constexpr int per = 256 / (D / 8);
-  return launch_dependent(sla::attend_sum_kernel<D>, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0,
-                          st, "attend_sum_kernel", a);
-}
-
-template <int D>
-sla_status launch_backward(const AttendPlan& w, const Maps& m, const AttendRowsArgs& r, AttendBwdArgs f,
-                           const AttendSpace& s, const int32_t* lens, cudaStream_t st) {
+sla_status launch_backward(const AttendPlan& w, const Maps& m, const AttendRowsArgs& r, const AttendBwdArgs& kv,
+                           const AttendBwdArgs& q, cudaStream_t st) {
   constexpr int per = 256 / (D / 8);
   SLA_TRY(launch_dependent(sla::attend_rows_kernel<D>, dim3(static_cast<unsigned>((r.rows + per - 1) / per)), dim3(256),
                            0, st, "attend_rows_kernel", r));
-  f.p = common_args(w, lens, s.err, w.dkv_splits, w.dkv_units);
-  f.part = s.dkv;
   constexpr int smem_kv = sla::AttendDkvSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dkv_kernel<D>, smem_kv));
-  SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(persistent_grid(w.dkv_units)), dim3(320), smem_kv, st,
-                           "attend_dkv_kernel", m.q, m.k, m.v, m.g, f));
-  f.p = common_args(w, lens, s.err, w.dq_splits, w.dq_units);
-  f.part = s.dq;
+  SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kThreads), smem_kv, st, "attend_dkv_kernel",
+                           m.q, m.k, m.v, m.g, kv));
   constexpr int smem_q = sla::AttendDqSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dq_kernel<D>, smem_q));
-  SLA_TRY(launch_dependent(sla::attend_dq_kernel<D>, dim3(persistent_grid(w.dq_units)), dim3(320), smem_q, st,
-                           "attend_dq_kernel", m.q, m.k, m.v, m.g, f));
-  if (w.dkv_splits > 1) {
-    SLA_TRY(launch_sum<D>(s.dkv, w.dkv_splits, w.p.Hk, w.p.Nk, w.k_rows, f.dk, st));
-    SLA_TRY(launch_sum<D>(s.dkv + w.dkv_splits * w.k_rows * D, w.dkv_splits, w.p.Hk, w.p.Nk, w.k_rows, f.dv, st));
+  SLA_TRY(launch_dependent(sla::attend_dq_kernel<D>, dim3(w.dq.ctas), dim3(sla::kThreads), smem_q, st, "attend_dq_kernel", m.q,
+                           m.k, m.v, m.g, q));
+  if (w.dkv.cut || w.dq.cut) {
+    const AttendSumArgs s{kv, q, w.dkv.ctas, w.dq.ctas};
+    const int ctas = w.dkv.ctas > w.dq.ctas ? w.dkv.ctas : w.dq.ctas;
+    SLA_TRY(launch_dependent(sla::attend_sum_kernel<D>, dim3(ctas, kTile / per, 3), dim3(256), 0, st,
+                             "attend_sum_kernel", s));
   }
-  if (w.dq_splits > 1) SLA_TRY(launch_sum<D>(s.dq, w.dq_splits, w.p.H, w.p.Nq, w.q_rows, f.dq, st));
   return SLA_OK;
 }
 
@@ -234,22 +261,18 @@ sla_status check_lens(const int32_t* lens) {
 extern "C" {
 
 size_t sla_workspace_size_attend(const sla_attend_problem* p) {
-  AttendPlan w;
-  if (make_plan(p, &w) != SLA_OK) return 0;
-  return layout(w, nullptr, false).bytes;
+  return space_bytes(p, false);
 }
 
 size_t sla_workspace_size_attend_backward(const sla_attend_problem* p) {
-  AttendPlan w;
-  if (make_plan(p, &w) != SLA_OK) return 0;
-  return layout(w, nullptr, true).bytes;
+  return space_bytes(p, true);
 }
 
 sla_status sla_attend(const sla_attend_problem* p, const sla_tensor* q, const sla_tensor* k, const sla_tensor* v,
                       const int32_t* kv_lens, const sla_tensor* out, float* lse, void* ws, size_t ws_bytes,
                       void* stream) {
   AttendPlan w;
-  SLA_TRY(make_plan(p, &w));
+  SLA_TRY(make_plan(p, kv_lens != nullptr, &w));
   SLA_TRY(check_operand("q", q, p->B, p->H, p->Nq));
   SLA_TRY(check_operand("k", k, p->B, p->Hk, p->Nk));
   SLA_TRY(check_operand("v", v, p->B, p->Hk, p->Nk));
@@ -259,9 +282,15 @@ sla_status sla_attend(const sla_attend_problem* p, const sla_tensor* q, const sl
   AttendSpace s;
   SLA_TRY(check_space(w, ws, ws_bytes, false, &s));
   Maps m;
-  SLA_TRY(input_maps(&m, w, q, k, v, nullptr));
+  const int tokens = w.narrow ? p->Nq : kTile;
+  SLA_TRY(query_map(&m.q, q, *p, tokens, w.heads));
+  SLA_TRY(operand_map(&m.k, k, p->B, p->Hk, p->Nk, p->D));
+  SLA_TRY(operand_map(&m.v, v, p->B, p->Hk, p->Nk, p->D));
   AttendFwdArgs f{};
-  f.p = common_args(w, kv_lens, s.err, w.fwd_splits, w.fwd_units);
+  f.p = common_args(w, kv_lens, s.err, w.fwd, s.meta);
+  f.narrow = w.narrow;
+  f.heads = w.heads;
+  f.q_bytes = tokens * w.heads * p->D * 2;
   f.out = row_out(out, p->B, p->H, p->Nq);
   f.lse = lse;
   f.part = s.part;
@@ -275,7 +304,7 @@ sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q,
                                const int32_t* kv_lens, const sla_tensor* dq, const sla_tensor* dk,
                                const sla_tensor* dv, void* ws, size_t ws_bytes, void* stream) {
   AttendPlan w;
-  SLA_TRY(make_plan(p, &w));
+  SLA_TRY(make_plan(p, kv_lens != nullptr, &w));
   SLA_TRY(check_operand("q", q, p->B, p->H, p->Nq));
   SLA_TRY(check_operand("k", k, p->B, p->Hk, p->Nk));
   SLA_TRY(check_operand("v", v, p->B, p->Hk, p->Nk));
@@ -289,20 +318,27 @@ sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q,
   AttendSpace s;
   SLA_TRY(check_space(w, ws, ws_bytes, true, &s));
   Maps m;
-  SLA_TRY(input_maps(&m, w, q, k, v, dO));
+  SLA_TRY(operand_map(&m.q, q, p->B, p->H, p->Nq, p->D));
+  SLA_TRY(operand_map(&m.k, k, p->B, p->Hk, p->Nk, p->D));
+  SLA_TRY(operand_map(&m.v, v, p->B, p->Hk, p->Nk, p->D));
+  SLA_TRY(operand_map(&m.g, dO, p->B, p->H, p->Nq, p->D));
   const RowOut o = row_out(out, p->B, p->H, p->Nq), g = row_out(dO, p->B, p->H, p->Nq);
   const AttendRowsArgs r{p->H, p->Nq, w.pad, static_cast<long long>(p->B) * p->H * w.pad,
                          o.p,  g.p,   o.sb,  o.sh, o.sn, g.sb, g.sh, g.sn, lse, s.nlse, s.ndelta};
   AttendBwdArgs f{};
+  f.p = common_args(w, kv_lens, s.err, w.dkv, s.meta);
+  f.part = s.part;
   f.nlse = s.nlse;
   f.ndelta = s.ndelta;
   f.pad = w.pad;
   f.dq = row_out(dq, p->B, p->H, p->Nq);
   f.dk = row_out(dk, p->B, p->Hk, p->Nk);
   f.dv = row_out(dv, p->B, p->Hk, p->Nk);
+  AttendBwdArgs fq = f;
+  fq.p = common_args(w, kv_lens, s.err, w.dq, s.meta_q);
+  fq.part = s.part_q;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return p->D == 128 ? launch_backward<128>(w, m, r, f, s, kv_lens, st)
-                     : launch_backward<64>(w, m, r, f, s, kv_lens, st);
+  return p->D == 128 ? launch_backward<128>(w, m, r, f, fq, st) : launch_backward<64>(w, m, r, f, fq, st);
 }
 
 }  // extern "C"

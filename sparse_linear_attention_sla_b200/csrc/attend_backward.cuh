@@ -26,7 +26,7 @@ struct AttendBwdArgs {
   const float* ndelta;  // [B * H, pad] -delta
   int pad;              // Nq rounded up to whole tiles
   RowOut dq, dk, dv;
-  float* part;          // splits > 1: dQ [splits][B * H * Nq][D], or dK then dV [splits][B * Hk * Nk][D]
+  float* part;          // parts of units (see AttendWork): dQ [2 * CTAs][128][D], or [2 * CTAs][dK, dV][128][D]
 };
 
 // -lse2 and -delta of every row, 8 channels a lane. Reads out and dO once (bound by HBM).
@@ -79,16 +79,16 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t* x) {
 
 // ---------------------------------------------------------------------------- dK, dV
 
-// One persistent CTA per SM, 320 threads, on units of 128 keys of one key head x a range of
-// the (query head of the group, query tile) pairs that see them:
+// One persistent CTA per SM, 384 threads, on units of 128 keys of one key head, a step being a
+// (query head of the group, query tile) that sees them:
 //   warp 0       TMA: K_j and V_j once, then Q_i, dO_i and the rows' statistics through a ring
 //                of two stages
-//   warp 1       tcgen05 issuer: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += T^T Q. The
-//                queue alternates: while the warps form P of tile i the tensor cores run
-//                dK of tile i - 1 and dP of tile i; while they form T, dV of tile i and S of
-//                tile i + 1.
-//   warps 2..9   thread = key row = TMEM lane; warps 2..5 take the tile's queries 0..63, warps
-//                6..9 queries 64..127
+//   warps 1, 3   tcgen05 issuers: S^T = K Q^T and dV += P^T dO; dP^T = V dO^T and dK += T^T Q. While the
+//                warps form P of tile i the tensor cores run dK of tile i - 1 and dP of tile i;
+//                while they form T, dV of tile i and S of tile i + 1.
+//   warp 2       scheduler: the CTA's units
+//   warps 4..11  thread = key row = TMEM lane; warps 4..7 take the tile's queries 0..63, warps
+//                8..11 queries 64..127
 // TMEM columns: S^T [0,128) and dP^T [128,256), each overwritten by its bf16 result (queries
 // 0..63 at +0, 64..127 at +64, so that each half of the warps overwrites only what it has
 // read); dV [256,256+D), dK [384,384+D).
@@ -102,32 +102,37 @@ struct AttendDkvSmem {
 };
 
 struct DkvUnit {
-  int b, hk, key0, split;
+  int b, hk, key0;
   int len, first;  // keys of the sequence; first query tile that sees a key of the tile
   int tiles;       // query tiles per head from there on
-  int lo, hi;      // this unit's range of group x tiles
   int dead;        // queries before this row see no key (causal, more queries than keys)
 };
 
 __device__ __forceinline__ DkvUnit dkv_unit(const AttendArgs& a, int u, bool record) {
   DkvUnit w;
   const int kt = tiles_of(a.Nk);
-  w.split = u % a.splits;
-  const int t = u / a.splits;
-  w.key0 = t % kt * kTile;
-  w.b = t / kt / a.Hk;
-  w.hk = t / kt % a.Hk;
+  w.key0 = u % kt * kTile;
+  w.b = u / kt / a.Hk;
+  w.hk = u / kt % a.Hk;
   w.len = attend_len(a, w.b, record);
   w.dead = a.causal ? max(0, a.Nq - w.len) : 0;
   const int first_row = a.causal ? max(0, w.key0 - (w.len - a.Nq)) : 0;  // sees key0, causal
   w.first = first_row / kTile;
   w.tiles = w.key0 < w.len && first_row < a.Nq ? tiles_of(a.Nq) - w.first : 0;
-  split_range(w.tiles * a.G, a.splits, w.split, w.lo, w.hi);
   return w;
 }
 
+// What the warps need of the current unit: n steps from lo on.
+struct DkvItem {
+  int b, hk, key0, len, first, tiles, dead, lo, n, slot;
+  __device__ __forceinline__ explicit DkvItem(const AttendItem& i)
+      : b(i.v[0]), hk(i.v[1]), key0(i.v[2]), len(i.v[3]), first(i.v[4]), tiles(i.v[5]), dead(i.v[6]), lo(i.v[7]),
+        n(tiles > 0 ? i.v[8] - lo : 0), slot(i.v[9]) {}
+  __device__ __forceinline__ bool stop() const { return b < 0; }
+};
+
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g,
                       const __grid_constant__ AttendBwdArgs f) {
@@ -142,42 +147,66 @@ __global__ void __launch_bounds__(320, 1)
   uint8_t* ring = sV + L::TILE;                                           // Q then dO
   float* stats = reinterpret_cast<float*>(ring + ST * L::STAGE);          // nlse[128] then ndelta[128]
 
-  __shared__ uint64_t kv_full, kv_free, s_full, dp_full, p_full, t_full, acc_full, acc_free, drain;
+  __shared__ uint64_t kv_full, kv_free, s_full, dp_full, p_full, t_full, acc_full[2], acc_free[2], drain;  // [dV, dK]
   __shared__ uint64_t q_full[ST], g_full[ST], q_free[ST], g_free[ST];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ ItemRing items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(&kv_full, 1);
-    mbar_init(&kv_free, 1);
+    mbar_init(&kv_free, 2);
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
     mbar_init(&p_full, 256);
     mbar_init(&t_full, 256);
-    mbar_init(&acc_full, 1);
-    mbar_init(&acc_free, 256);
-    mbar_init(&drain, 1);
+    mbar_init(&acc_full[0], 1);
+    mbar_init(&acc_full[1], 1);
+    mbar_init(&acc_free[0], 128);
+    mbar_init(&acc_free[1], 128);
+    mbar_init(&drain, 2);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&g_full[s], 1);
-      mbar_init(&q_free[s], 1);
-      mbar_init(&g_free[s], 1);
+      mbar_init(&q_free[s], 2);
+      mbar_init(&g_free[s], 2);
     }
+    items.init();
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
+  grid_dep_wait();
+  const auto steps = [&](int u) { return dkv_unit(a, u, false).tiles * a.G; };
+  AttendWork work = attend_work(a, steps, kThreads);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
-  grid_dep_wait();
+  constexpr uint32_t tmem = 0;  // all columns are allocated
+  AttendItem item;
 
-  if (warp == 0) {
+  if (warp < 4) regs_down<kIssueRegs>();
+  if (warp == kScheduleWarp) {
+    if (lane == 0) {
+      uint32_t ni = 0;
+      int u, lo, hi, n, to;
+      bool ok = true;
+      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+        note_part(a, work, u, lo, hi, n, to);
+        const DkvUnit w = dkv_unit(a, u, true);
+        item = {w.b, w.hk, w.key0, w.len, w.first, w.tiles, w.dead, lo, hi, part_slot(lo, hi, n)};
+        ok = items.put(ni++, item, a.err, &abort_flag);
+      }
+      item.v[0] = -1;
+      if (ok) items.put(ni, item, a.err, &abort_flag);
+    }
+    __syncwarp();
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ TMA producer
+    uint32_t ni = 0;
     if (lane == 0) {
       prefetch_tmap(&map_q);
       prefetch_tmap(&map_k);
@@ -185,15 +214,17 @@ __global__ void __launch_bounds__(320, 1)
       prefetch_tmap(&map_g);
       uint32_t nr = 0, nu = 0, ng = 0;  // Q tiles, units and dO tiles loaded
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-        const DkvUnit w = dkv_unit(a, u, true);
-        if (w.lo >= w.hi) continue;
+      while (ok) {
+        if (!(ok = items.get_one(ni++, item, a.err, &abort_flag))) break;
+        const DkvItem w(item);
+        if (w.stop()) break;
+        if (w.n == 0) continue;
         if (nu > 0 && !(ok = mbar_wait(&kv_free, (nu - 1) & 1, a.err, &abort_flag))) break;
         mbar_arrive_expect_tx(&kv_full, 2 * L::TILE);
         for (int b = 0; b < DB; ++b) tma_load_4d(sK + b * kBox, &map_k, &kv_full, b * 64, w.key0, w.hk, w.b);
         for (int b = 0; b < DB; ++b) tma_load_4d(sV + b * kBox, &map_v, &kv_full, b * 64, w.key0, w.hk, w.b);
         ++nu;
-        for (int i = w.lo; i < w.hi; ++i) {
+        for (int i = w.lo; i < w.lo + w.n; ++i) {
           const int h = w.hk * a.G + i / w.tiles, row = (w.first + i % w.tiles) * kTile;
           const uint32_t s = nr % ST, r = nr / ST;
           if (r > 0 && !(ok = mbar_wait(&q_free[s], (r - 1) & 1, a.err, &abort_flag))) break;
@@ -219,95 +250,79 @@ __global__ void __launch_bounds__(320, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t k0 = smem_u32(sK), v0 = smem_u32(sV), r0 = smem_u32(ring);
-    uint32_t it = 0, nu = 0;  // query tiles and units so far
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
+    // ------------------------------------------------------------ MMA issuers
+    // The first warp: S^T(i) = K Q_i^T, then dV += P(i)^T dO_i. The second: dP^T(i) = V dO_i^T, then dK +=
+    // T(i)^T Q_i. Each chain's own order keeps S^T(i + 1) from overwriting P(i), and dP^T(i + 1) T(i).
+    const int y = warp == kMmaWarp2;
+    const uint32_t a0 = smem_u32(y ? sV : sK), r0 = smem_u32(ring);
+    const uint32_t col = y ? TP : 0, acc = y ? TK : TV;  // TMEM columns of the products
+    const uint32_t one = y ? L::TILE : 0, two = y ? 0 : L::TILE;  // first and second product's tile in a stage
+    uint32_t nu = 0, ni = 0;
+    RingPos pos;           // of the first product's tile
+    uint32_t done = 0;     // parity of the next P or T
     bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
+    const uint32_t lead = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
+    auto issue_first = [&](bool last) -> bool {
+      const uint32_t s = pos.s;
+      if (!wait(y ? &g_full[s] : &q_full[s], pos.parity)) return false;
+      tc_fence_after();
+      issue_ss<D, 128>(lead, col, a0, r0 + s * L::STAGE + one);
+      mma_commit(lead, y ? &dp_full : &s_full);
+      mma_commit(lead, y ? &g_free[s] : &q_free[s]);
+      if (last) mma_commit(lead, &kv_free);  // the unit's last reader of K_j or V_j
+      pos.next(ST);
+      return true;
     };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const DkvUnit w = dkv_unit(a, u, false);
-      const int n = w.hi - w.lo;
-      if (n <= 0) continue;
-      // Rows of the unit's query tile i that see no key may hold anything: zero them where the
-      // products sum over rows.
-      auto clean = [&](uint8_t* tile, int i) {
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const DkvItem w(item);
+      if (w.stop()) break;
+      const int n = w.n;
+      if (n == 0) continue;
+      if (!(ok = wait(&kv_full, nu & 1))) break;
+      RingPos cur = pos;  // of the second product's tile
+      if (!(ok = issue_first(n == 1))) break;
+      if (nu > 0 && !(ok = wait(&acc_free[y], (nu - 1) & 1))) break;
+      for (int i = 0; i < n; ++i) {
+        if (!(ok = wait(y ? &t_full : &p_full, done))) break;
+        done ^= 1;
+        uint8_t* tile = ring + cur.s * L::STAGE + two;
+        if (!(ok = wait(y ? &q_full[cur.s] : &g_full[cur.s], cur.parity))) break;
+        // Rows that see no key may hold anything: zero them where the product sums over rows.
         const int row = (w.first + (w.lo + i) % w.tiles) * kTile;
         if (row < w.dead) zero_rows<D>(tile, 0, min(kTile, w.dead - row));
-      };
-      auto issue_s = [&](int i) -> bool {
-        const uint32_t t = it + i, s = t % ST;
-        if (!wait_all(&q_full[s], (t / ST) & 1)) return false;
-        clean(ring + s * L::STAGE, i);
         tc_fence_after();
-        if (elect_one()) {
-          issue_ss<D>(tmem, k0, r0 + s * L::STAGE);
-          umma_commit(&s_full);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_dp = [&](int i) -> bool {
-        const uint32_t t = it + i, s = t % ST;
-        if (!wait_all(&g_full[s], (t / ST) & 1)) return false;
-        clean(ring + s * L::STAGE + L::TILE, i);
-        tc_fence_after();
-        if (elect_one()) {
-          issue_ss<D>(tmem + TP, v0, r0 + s * L::STAGE + L::TILE);
-          umma_commit(&dp_full);
-          if (i + 1 == n) umma_commit(&kv_free);  // the unit's last reader of K_j and V_j
-        }
-        __syncwarp();
-        return true;
-      };
-      if (!(ok = wait_all(&kv_full, nu & 1))) break;
-      if (!(ok = issue_s(0) && issue_dp(0))) break;
-      if (nu > 0 && !(ok = wait_all(&acc_free, (nu - 1) & 1))) break;
-      for (int i = 0; i < n; ++i) {
-        const uint32_t t = it + i, s = t % ST;
-        const uint32_t q = r0 + s * L::STAGE, g = q + L::TILE;
-        if (!(ok = wait_all(&p_full, t & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_ts<D, 64>(tmem + TV, tmem, g, i > 0);
-          umma_commit(&g_free[s]);
-        }
-        __syncwarp();
-        if (i + 1 < n && !(ok = issue_s(i + 1))) break;
-        if (!(ok = wait_all(&t_full, t & 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_ts<D, 64>(tmem + TK, tmem + TP, q, i > 0);
-          umma_commit(&q_free[s]);
-          if (i + 1 == n) umma_commit(&acc_full);
-        }
-        __syncwarp();
-        if (i + 1 < n && !(ok = issue_dp(i + 1))) break;
+        issue_ts<D, 0, 8, 64>(lead, acc, col, smem_u32(tile), i > 0);
+        mma_commit(lead, y ? &q_free[cur.s] : &g_free[cur.s]);
+        if (i + 1 == n) mma_commit(lead, &acc_full[y]);
+        cur.next(ST);
+        if (i + 1 < n && !(ok = issue_first(i + 2 == n))) break;
       }
-      it += n;
       ++nu;
     }
-    if (elect_one()) umma_commit(&drain);
-    __syncwarp();
+    mma_commit(lead, &drain);
     mbar_wait(&drain, 0, nullptr, nullptr);
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ P and T, then the epilogue
-    const int half = warp >= 6;
+    regs_up<kComputeRegs>();
+    const int half = warp >= 8;
     const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + half * 64, p_addr = lane_addr + TP + half * 64;
     const float sc = a.scale_log2;
     const uint64_t sc2 = f2_make(sc, sc);
-    uint32_t it = 0, nu = 0;
+    uint32_t it = 0, nu = 0, ni = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
+      return warp_wait(bar, parity, a.err, &abort_flag);
     };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const DkvUnit w = dkv_unit(a, u, false);
-      const int n = w.hi - w.lo;
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const DkvItem w(item);
+      if (w.stop()) break;
+      const int n = w.n;
       const int key = w.key0 + r;
       for (int i = 0; i < n; ++i, ++it) {
         const int row = (w.first + (w.lo + i) % w.tiles) * kTile + half * 64;  // first query of this half
@@ -372,16 +387,15 @@ __global__ void __launch_bounds__(320, 1)
         mbar_arrive(&t_full);
       }
       if (!ok) break;
-      // Warps 2..5 write dV, warps 6..9 dK (times scale); zeros where no query saw the keys.
+      // Warps 4..7 write dV, warps 8..11 dK (times scale); zeros where no query saw the keys.
       if (n > 0) {
-        if (!(ok = wait(&acc_full, nu & 1))) break;
+        if (!(ok = wait(&acc_full[half], nu & 1))) break;
         tc_fence_after();
       }
       const RowOut& o = half ? f.dk : f.dv;
       const float mul = half ? a.scale : 1.f;
-      const size_t rows = static_cast<size_t>(a.B) * a.Hk * a.Nk;
-      const size_t at = (static_cast<size_t>(w.b) * a.Hk + w.hk) * a.Nk + key;
-      float* part = f.part + ((half ? 0 : static_cast<size_t>(a.splits)) + w.split) * rows * D + at * D;
+      const int slot = w.slot;
+      float* part = f.part + ((static_cast<size_t>(slot) * 2 + (half ? 0 : 1)) * kTile + r) * D;
       __nv_bfloat16* out = o.p + w.b * o.sb + w.hk * o.sh + key * o.sn;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(320, 1)
           for (int c = 0; c < 32; ++c) x[c] = 0u;
         }
         if (key < a.Nk) {
-          if (a.splits == 1)
+          if (slot < 0)
             store_row32(out + c0, x, mul, o.wide);
           else
             store_row32(part + c0, x, mul, true);
@@ -403,28 +417,29 @@ __global__ void __launch_bounds__(320, 1)
       }
       if (n > 0) {
         tc_fence_before();
-        mbar_arrive(&acc_free);
+        mbar_arrive(&acc_free[half]);
         ++nu;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem_base_sh, 512);
   }
 }
 
 // ---------------------------------------------------------------------------- dQ
 
-// One persistent CTA per SM, 320 threads, on units of 128 query rows of one head x a range of
-// key tiles:
+// One persistent CTA per SM, 384 threads, on units of 128 query rows of one head, a step being a
+// key tile:
 //   warp 0       TMA: Q_i and dO_i once, then K_j and V_j through a ring of two stages
-//   warp 1       tcgen05 issuer: S = Q K^T (two TMEM buffers), dP = dO V^T, dQ += T K. S of
-//                tile j + 1 and dP of tile j + 1 run while the warps form T of tile j.
-//   warps 2..9   thread = query row = TMEM lane; warps 2..5 take the tile's keys 0..63, warps
-//                6..9 keys 64..127
+//   warps 1, 3   tcgen05 issuers: S = Q K^T (two TMEM buffers) and dQ += T K; dP = dO V^T. S and dP of
+//                tile j + 1 run while the warps form T of tile j.
+//   warp 2       scheduler: the CTA's units
+//   warps 4..11  thread = query row = TMEM lane; warps 4..7 take the tile's keys 0..63, warps
+//                8..11 keys 64..127
 // TMEM columns: S ping-pong [0,128) [128,256) (T, bf16, over it: keys 0..63 at +0, 64..127 at
 // +64), dP [256,384), dQ [384,384+D).
 template <int D>
@@ -435,28 +450,30 @@ struct AttendDqSmem {
 };
 
 struct DqUnit {
-  int b, h, row0, split;
-  int len, lo, n;  // keys of the sequence; first key tile and key tiles of this unit
+  int b, h, row0;
+  int len, tiles;  // keys of the sequence; key tiles that the unit's rows see
 };
 
 __device__ __forceinline__ DqUnit dq_unit(const AttendArgs& a, int u, bool record) {
   DqUnit w;
   const int qt = tiles_of(a.Nq);
-  w.split = u % a.splits;
-  const int t = u / a.splits;
-  const int i = t % qt;
-  w.row0 = (a.causal ? qt - 1 - i : i) * kTile;  // causal: the longest rows first
-  w.b = t / qt / a.H;
-  w.h = t / qt % a.H;
+  w.row0 = u % qt * kTile;
+  w.b = u / qt / a.H;
+  w.h = u / qt % a.H;
   w.len = attend_len(a, w.b, record);
-  int hi;
-  split_range(tiles_of(attend_key_end(a, w.len, min(w.row0 + kTile, a.Nq) - 1)), a.splits, w.split, w.lo, hi);
-  w.n = hi - w.lo;
+  w.tiles = tiles_of(attend_key_end(a, w.len, min(w.row0 + kTile, a.Nq) - 1));
   return w;
 }
 
+struct DqItem {
+  int b, h, row0, len, lo, n, slot;
+  __device__ __forceinline__ explicit DqItem(const AttendItem& i)
+      : b(i.v[0]), h(i.v[1]), row0(i.v[2]), len(i.v[3]), lo(i.v[4]), n(i.v[5]), slot(i.v[6]) {}
+  __device__ __forceinline__ bool stop() const { return b < 0; }
+};
+
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g,
                      const __grid_constant__ AttendBwdArgs f) {
@@ -475,16 +492,17 @@ __global__ void __launch_bounds__(320, 1)
   __shared__ uint64_t k_full[ST], v_full[ST], k_free[ST], v_free[ST];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ ItemRing items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(&q_full, 1);
-    mbar_init(&q_free, 1);
+    mbar_init(&q_free, 2);
     mbar_init(&dp_full, 1);
     mbar_init(&dp_free, 256);
     mbar_init(&acc_full, 1);
     mbar_init(&acc_free, 256);
-    mbar_init(&drain, 1);
+    mbar_init(&drain, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&t_full[s], 256);
@@ -495,20 +513,41 @@ __global__ void __launch_bounds__(320, 1)
       mbar_init(&k_free[s], 1);
       mbar_init(&v_free[s], 1);
     }
+    items.init();
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
+  grid_dep_wait();
+  const auto steps = [&](int u) { return dq_unit(a, u, false).tiles; };
+  AttendWork work = attend_work(a, steps, kThreads);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
-  grid_dep_wait();
+  constexpr uint32_t tmem = 0;  // all columns are allocated
+  AttendItem item;
 
-  if (warp == 0) {
+  if (warp < 4) regs_down<kIssueRegs>();
+  if (warp == kScheduleWarp) {
+    if (lane == 0) {
+      uint32_t ni = 0;
+      int u, lo, hi, n, to;
+      bool ok = true;
+      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+        note_part(a, work, u, lo, hi, n, to);
+        const DqUnit w = dq_unit(a, u, true);
+        item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n)};
+        ok = items.put(ni++, item, a.err, &abort_flag);
+      }
+      item.v[0] = -1;
+      if (ok) items.put(ni, item, a.err, &abort_flag);
+    }
+    __syncwarp();
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ TMA producer
+    uint32_t ni = 0;
     if (lane == 0) {
       prefetch_tmap(&map_q);
       prefetch_tmap(&map_k);
@@ -516,16 +555,18 @@ __global__ void __launch_bounds__(320, 1)
       prefetch_tmap(&map_g);
       uint32_t nk = 0, nv = 0, nu = 0;  // K tiles, V tiles and units loaded
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-        const DqUnit w = dq_unit(a, u, true);
-        if (w.n <= 0) continue;
+      while (ok) {
+        if (!(ok = items.get_one(ni++, item, a.err, &abort_flag))) break;
+        const DqItem w(item);
+        if (w.stop()) break;
+        if (w.n == 0) continue;
         if (nu > 0 && !(ok = mbar_wait(&q_free, (nu - 1) & 1, a.err, &abort_flag))) break;
         mbar_arrive_expect_tx(&q_full, 2 * L::TILE);
         for (int b = 0; b < DB; ++b) tma_load_4d(sQ + b * kBox, &map_q, &q_full, b * 64, w.row0, w.h, w.b);
         for (int b = 0; b < DB; ++b) tma_load_4d(sG + b * kBox, &map_g, &q_full, b * 64, w.row0, w.h, w.b);
         ++nu;
-        for (int j = 0; j < w.n; ++j) {
-          const int key = (w.lo + j) * kTile;
+        for (int j = w.lo; j < w.lo + w.n; ++j) {
+          const int key = j * kTile;
           const uint32_t s = nk % ST, r = nk / ST;
           if (r > 0 && !(ok = mbar_wait(&k_free[s], (r - 1) & 1, a.err, &abort_flag))) break;
           mbar_arrive_expect_tx(&k_full[s], L::TILE);
@@ -546,87 +587,97 @@ __global__ void __launch_bounds__(320, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t q0 = smem_u32(sQ), g0 = smem_u32(sG), rk = smem_u32(ringK), rv = smem_u32(ringV);
-    uint32_t it = 0, nu = 0;  // key tiles and units so far
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer of S and dQ
+    const uint32_t q0 = smem_u32(sQ), rk = smem_u32(ringK);
+    uint32_t it = 0, nu = 0, ni = 0;  // key tiles, units with work and items so far
+    RingPos pos;                      // of the next S's K tile
     bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
-    };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const DqUnit w = dq_unit(a, u, false);
+    const uint32_t lead = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const DqItem w(item);
+      if (w.stop()) break;
       const int n = w.n;
-      if (n <= 0) continue;
+      if (n == 0) continue;
       auto issue_s = [&](int j) -> bool {
-        const uint32_t t = it + j, s = t % ST;
-        if (!wait_all(&k_full[s], (t / ST) & 1)) return false;
+        const uint32_t s = pos.s, t = it + j;
+        if (!wait(&k_full[s], pos.parity)) return false;
         const int keys = w.len - (w.lo + j) * kTile;  // real keys of the tile
         if (keys < kTile) zero_rows<D>(ringK + s * L::TILE, keys, kTile);
         tc_fence_after();
-        if (elect_one()) {
-          issue_ss<D>(tmem + (t & 1) * 128, q0, rk + s * L::TILE);
-          umma_commit(&s_full[t & 1]);
-        }
-        __syncwarp();
+        issue_ss<D, 128>(lead, (t & 1) * 128, q0, rk + s * L::TILE);
+        mma_commit(lead, &s_full[t & 1]);
+        if (j + 1 == n) mma_commit(lead, &q_free);  // the unit's last reader of Q_i
+        pos.next(ST);
         return true;
       };
-      auto issue_dp = [&](int j) -> bool {
-        const uint32_t t = it + j, s = t % ST;
-        if (!wait_all(&v_full[s], (t / ST) & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_ss<D>(tmem + TP, g0, rv + s * L::TILE);
-          umma_commit(&dp_full);
-          umma_commit(&v_free[s]);
-          if (j + 1 == n) umma_commit(&q_free);  // the unit's last reader of Q_i and dO_i
-        }
-        __syncwarp();
-        return true;
-      };
-      if (!(ok = wait_all(&q_full, nu & 1))) break;
+      if (!(ok = wait(&q_full, nu & 1))) break;
+      RingPos cur = pos;  // of dQ's K tile
       if (!(ok = issue_s(0))) break;
-      // dP's columns: the previous unit's last dP has been read
-      if (it > 0 && !(ok = wait_all(&dp_free, (it - 1) & 1))) break;
-      if (!(ok = issue_dp(0))) break;
+      if (nu > 0 && !(ok = wait(&acc_free, (nu - 1) & 1))) break;
       for (int j = 0; j < n; ++j) {
-        const uint32_t t = it + j, s = t % ST;
-        if (j + 1 < n) {
-          if (!(ok = issue_s(j + 1))) break;
-          if (!(ok = wait_all(&dp_free, t & 1))) break;
-          tc_fence_after();
-          if (!(ok = issue_dp(j + 1))) break;
-        }
-        if (j == 0 && nu > 0 && !(ok = wait_all(&acc_free, (nu - 1) & 1))) break;
-        if (!(ok = wait_all(&t_full[t & 1], (t >> 1) & 1))) break;
+        const uint32_t t = it + j;
+        if (j + 1 < n && !(ok = issue_s(j + 1))) break;
+        if (!(ok = wait(&t_full[t & 1], (t >> 1) & 1))) break;
         tc_fence_after();
-        if (elect_one()) {
-          issue_ts<D, 64>(tmem + TQ, tmem + (t & 1) * 128, rk + s * L::TILE, j > 0);
-          umma_commit(&k_free[s]);
-          if (j + 1 == n) umma_commit(&acc_full);
-        }
-        __syncwarp();
+        issue_ts<D, 0, 8, 64>(lead, TQ, (t & 1) * 128, rk + cur.s * L::TILE, j > 0);
+        mma_commit(lead, &k_free[cur.s]);
+        if (j + 1 == n) mma_commit(lead, &acc_full);
+        cur.next(ST);
       }
       it += n;
       ++nu;
     }
-    if (elect_one()) umma_commit(&drain);
-    __syncwarp();
+    mma_commit(lead, &drain);
     mbar_wait(&drain, 0, nullptr, nullptr);
-  } else {
+  } else if (warp == kMmaWarp2) {
+    // ------------------------------------------------------------ MMA issuer of dP
+    const uint32_t g0 = smem_u32(sG), rv = smem_u32(ringV);
+    uint32_t it = 0, nu = 0, ni = 0;
+    RingPos pos;
+    bool ok = true;
+    const uint32_t lead = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const DqItem w(item);
+      if (w.stop()) break;
+      if (w.n == 0) continue;
+      if (!(ok = wait(&q_full, nu & 1))) break;
+      for (int j = 0; j < w.n; ++j, ++it) {
+        const uint32_t s = pos.s;
+        if (!(ok = wait(&v_full[s], pos.parity))) break;
+        if (it > 0 && !(ok = wait(&dp_free, (it - 1) & 1))) break;  // the previous dP has been read
+        tc_fence_after();
+        issue_ss<D, 128>(lead, TP, g0, rv + s * L::TILE);
+        mma_commit(lead, &dp_full);
+        mma_commit(lead, &v_free[s]);
+        if (j + 1 == w.n) mma_commit(lead, &q_free);  // the unit's last reader of dO_i
+        pos.next(ST);
+      }
+      ++nu;
+    }
+    mma_commit(lead, &drain);
+    mbar_wait(&drain, 0, nullptr, nullptr);
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ T, then the epilogue
-    const int half = warp >= 6;
+    regs_up<kComputeRegs>();
+    const int half = warp >= 8;
     const int r = (warp & 3) * 32 + lane;  // query row of the tile = TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sc = a.scale_log2;
     const uint64_t sc2 = f2_make(sc, sc);
-    uint32_t it = 0, nu = 0;
+    uint32_t it = 0, nu = 0, ni = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.err, &abort_flag));
+      return warp_wait(bar, parity, a.err, &abort_flag);
     };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const DqUnit w = dq_unit(a, u, false);
+    while (ok) {
+      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      const DqItem w(item);
+      if (w.stop()) break;
       const int n = w.n;
       const int row = w.row0 + r;
       const int end = attend_key_end(a, w.len, row);
@@ -684,9 +735,8 @@ __global__ void __launch_bounds__(320, 1)
         if (!(ok = wait(&acc_full, nu & 1))) break;
         tc_fence_after();
       }
-      // scale times the accumulator: warps 2..5 its first D / 2 channels, warps 6..9 the rest
-      const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
-      const size_t o = (static_cast<size_t>(w.b) * a.H + w.h) * a.Nq + row;
+      // scale times the accumulator: warps 4..7 its first D / 2 channels, warps 8..11 the rest
+      const int slot = w.slot;
 #pragma unroll 1
       for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
         uint32_t x[32];
@@ -698,10 +748,10 @@ __global__ void __launch_bounds__(320, 1)
           for (int c = 0; c < 32; ++c) x[c] = 0u;
         }
         if (row < a.Nq) {
-          if (a.splits == 1)
+          if (slot < 0)
             store_row32(f.dq.p + w.b * f.dq.sb + w.h * f.dq.sh + row * f.dq.sn + c0, x, a.scale, f.dq.wide);
           else
-            store_row32(f.part + (w.split * rows + o) * D + c0, x, a.scale, true);
+            store_row32(f.part + (static_cast<size_t>(slot) * kTile + r) * D + c0, x, a.scale, true);
         }
         __syncwarp();
       }
@@ -714,36 +764,55 @@ __global__ void __launch_bounds__(320, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem_base_sh, 512);
   }
 }
 
-// Sum of the splits' fp32 rows in ascending order, rounded once: out [B, H, N, D].
+// Joins the parts that attend_dkv_kernel (blockIdx.z 0: dK, 1: dV) and attend_dq_kernel (2) left: for the unit
+// that CTA blockIdx.x began and others went on with, the sum of the parts' rows in ascending CTA
+// order, rounded once. 8 channels a thread.
 struct AttendSumArgs {
-  const float* part;  // [splits][rows][D]
-  int splits, H, N;
-  long long rows;     // B * H * N
-  RowOut out;
+  AttendBwdArgs kv, q;
+  int kv_ctas, q_ctas;
 };
 
 template <int D>
-__global__ void __launch_bounds__(256) attend_sum_kernel(AttendSumArgs a) {
+__global__ void __launch_bounds__(256) attend_sum_kernel(const __grid_constant__ AttendSumArgs s) {
   constexpr int T = D / 8;
-  const long long i = static_cast<long long>(blockIdx.x) * (256 / T) + threadIdx.x / T;
-  const int c = (threadIdx.x % T) * 8;
   grid_dep_wait();
-  if (i >= a.rows) return;
-  float s[8] = {};
-  for (int k = 0; k < a.splits; ++k) {
-    const float4* p = reinterpret_cast<const float4*>(a.part + (k * a.rows + i) * D + c);
-    const float4 x = p[0], y = p[1];
-    s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w, s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+  const bool is_q = blockIdx.z == 2;
+  const AttendBwdArgs& f = is_q ? s.q : s.kv;
+  const AttendArgs& a = f.p;
+  const int C = is_q ? s.q_ctas : s.kv_ctas, c0 = blockIdx.x;
+  if (c0 >= C || !a.meta) return;
+  const int4 meta = a.meta[c0];
+  if (meta.x < 0) return;
+  const int r = blockIdx.y * (256 / T) + threadIdx.x / T, c = (threadIdx.x % T) * 8;
+  const RowOut& o = is_q ? f.dq : blockIdx.z == 0 ? f.dk : f.dv;
+  __nv_bfloat16* out;
+  if (is_q) {
+    const DqUnit w = dq_unit(a, meta.x, false);
+    if (w.row0 + r >= a.Nq) return;
+    out = o.p + w.b * o.sb + w.h * o.sh + (w.row0 + r) * o.sn + c;
+  } else {
+    const DkvUnit w = dkv_unit(a, meta.x, false);
+    if (w.key0 + r >= a.Nk) return;
+    out = o.p + w.b * o.sb + w.hk * o.sh + (w.key0 + r) * o.sn + c;
   }
-  const long long bh = i / a.N;
-  *reinterpret_cast<uint4*>(a.out.p + (bh / a.H) * a.out.sb + (bh % a.H) * a.out.sh + (i % a.N) * a.out.sn + c) =
-      make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+  float x[8] = {};
+#pragma unroll 4
+  for (int k = c0; k <= meta.y; ++k) {
+    if (part_is_empty(meta.z, C, k)) continue;
+    size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k);
+    if (!is_q) at = at * 2 + blockIdx.z;
+    const float4* p = reinterpret_cast<const float4*>(f.part + (at * kTile + r) * D + c);
+    const float4 u = p[0], v = p[1];
+    x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w, x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
+  }
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 }  // namespace sla

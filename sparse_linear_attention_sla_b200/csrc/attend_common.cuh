@@ -3,8 +3,8 @@
 //
 // All of them work on tiles of 128 rows x D channels in shared memory: D / 64 boxes of 128
 // rows x 128 bytes in TMA's 128-byte swizzle. Two kinds of product cover forward and backward:
-//   ss: D[128 x 128] = A B^T over D channels, both tiles read as rows x channels (K-major)
-//   ts: D[128 x D] (+)= P B over 128 rows, P (bf16) in TMEM, B read row by row (MN-major)
+//   ss: D[128 x 128 or 64] = A B^T over D channels, both tiles read as rows x channels (K-major)
+//   ts: D[128 x D] (+)= P B over 64 or 128 rows, P (bf16) in TMEM, B read row by row (MN-major)
 #pragma once
 
 #include "sm100.cuh"
@@ -14,12 +14,28 @@ namespace sla {
 struct AttendArgs {
   int B, H, Hk, G, Nq, Nk;  // G = H / Hk query heads share a key head
   int causal;
-  int splits;
-  int units;                // work items of the launch
   float scale, scale_log2;  // scale, scale * log2(e)
   const int32_t* lens;      // [B] keys of each sequence, or null (Nk)
   uint32_t* err;
+  // the launch's work items (see AttendWork)
+  int units;
+  int waves;    // units c, c + gridDim.x, ... that CTA c takes whole, this many of them
+  int uniform;  // every unit has the same number of steps
+  int4* meta;   // [gridDim.x] what attend_join_kernel / attend_sum_kernel join (null: nothing is cut)
 };
+
+// Blocks of three warpgroups: the first holds the TMA and the MMA warp, the other two the warps
+// that compute. 384 threads are launched with 168 registers each (64512); the first warpgroup
+// keeps 88 and the others take 208: 128 * (88 + 2 * 208) = 64512.
+constexpr int kThreads = 384;
+constexpr int kIssueRegs = 88, kComputeRegs = 208;
+static_assert(128 * (kIssueRegs + 2 * kComputeRegs) <= kThreads * 168, "more registers than the block has");
+
+// The first warpgroup's warps. Two issue MMAs, each its own chain of products: what one warp needs to
+// wait for a barrier, issue eight MMAs and commit them is over 1000 cycles, about what the tensor
+// cores need for them.
+constexpr int kProducerWarp = 0, kMmaWarp = 1, kScheduleWarp = 2, kMmaWarp2 = 3;
+constexpr int kItemReaders = 11;  // the producer, the MMA warps and the eight computing warps
 
 constexpr int kTile = 128;                 // rows of every tile
 constexpr uint32_t kBox = kTile * 128;     // bytes of one 64-channel box
@@ -42,36 +58,274 @@ __device__ __forceinline__ int attend_key_end(const AttendArgs& a, int len, int 
 
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
-// The part [lo, hi) of n tiles that split s of a.splits takes.
-__device__ __forceinline__ void split_range(int n, int splits, int s, int& lo, int& hi) {
-  const int per = (n + splits - 1) / splits;
-  lo = min(n, s * per);
-  hi = min(n, lo + per);
+// How a launch's units are shared out. CTA c first takes `waves` whole units c, c + C, ...
+// (neighbouring CTAs work on neighbouring units, so a head's tiles stay in L2). The steps of all
+// units behind those are laid end to end, each unit followed by kUnitCost steps that stand for
+// its loads and its epilogue, and cut into C equal ranges, one per CTA: every CTA gets the same
+// work whatever the lengths are, and at most its first and last unit is a part of one. A part
+// (steps [lo, hi) of n) is written as fp32 rows into slot 2c (it continues a unit) or 2c + 1 (it
+// begins one) and joined afterwards in ascending CTA order. A unit without steps counts as one.
+constexpr int kUnitCost = 2;
+
+struct AttendWork {
+  int k, u, off, left;
+  long long end, total;  // of the range, and all steps
+
+  // The next unit u_ and the steps [lo, hi) of its n that this CTA takes; `to` is where its range
+  // ends, in steps from the unit's first.
+  template <class Steps>
+  __device__ __forceinline__ bool next(const AttendArgs& a, const Steps& steps, int& u_, int& lo, int& hi, int& n,
+                                       int& to) {
+    if (k < a.waves) {
+      u_ = blockIdx.x + k * gridDim.x;
+      ++k;
+      if (u_ >= a.units) return false;
+      lo = 0;
+      hi = n = to = max(1, steps(u_));
+      return true;
+    }
+    while (left > 0) {
+      u_ = u++;
+      n = max(1, steps(u_));
+      lo = off;
+      to = min(n + kUnitCost, off + left);
+      left -= to - off;
+      off = 0;
+      hi = min(n, to);
+      if (lo < hi) return true;
+    }
+    return false;
+  }
+};
+
+// Run by all `threads` (a multiple of 32, at most 1024) threads of the block before its roles
+// part: this CTA's range. Thread 0 clears the CTA's entry of meta.
+template <class Steps>
+__device__ __forceinline__ AttendWork attend_work(const AttendArgs& a, const Steps& steps, int threads) {
+  __shared__ int warp_sum[32];
+  __shared__ int found[2];
+  const int C = gridDim.x, c = blockIdx.x, tid = threadIdx.x;
+  const int base = min(a.units, a.waves * C), R = a.units - base;
+  AttendWork w{0, 0, 0, 0, 0, 0};
+  if (tid == 0 && a.meta) a.meta[c] = make_int4(-1, 0, 0, 0);
+  if (R == 0) return w;
+  long long total, start, end;
+  if (a.uniform) {
+    const int n = max(1, steps(base)) + kUnitCost;
+    total = static_cast<long long>(R) * n;
+    start = total * c / C;
+    end = total * (c + 1) / C;
+    w.u = base + static_cast<int>(start / n);
+    w.off = static_cast<int>(start % n);
+  } else {
+    // Each thread sums a run of units; a scan over the block gives the runs' places.
+    const int run = (R + threads - 1) / threads;
+    const int lo = base + min(R, tid * run), hi = base + min(R, (tid + 1) * run);
+    int sum = 0;
+    for (int u = lo; u < hi; ++u) sum += max(1, steps(u)) + kUnitCost;
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if ((tid & 31) >= o) scan += v;
+    }
+    if ((tid & 31) == 31) warp_sum[tid >> 5] = scan;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < threads / 32; ++i) {
+      if (i < (tid >> 5)) before += warp_sum[i];
+      all += warp_sum[i];
+    }
+    total = all;
+    start = total * c / C;
+    end = total * (c + 1) / C;
+    int at = before + scan - sum;  // this run's place
+    if (start >= at && start < at + sum) {
+      for (int u = lo; u < hi; ++u) {
+        const int n = max(1, steps(u)) + kUnitCost;
+        if (start < at + n) {
+          found[0] = u;
+          found[1] = static_cast<int>(start) - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    w.u = found[0];
+    w.off = found[1];
+  }
+  w.left = static_cast<int>(end - start);
+  w.end = end;
+  w.total = total;
+  return w;
 }
 
-// One lane of the MMA warp issues. D[128 x 128] = A B^T over D channels.
-template <int D>
-__device__ __forceinline__ void issue_ss(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
-  constexpr uint32_t id = idesc_bf16_f32(128, 128, 0, 0);
+// A whole warp waits; all lanes get the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort_flag));
+}
+
+// The unit that a CTA works on, as its scheduler warp passes it to the other warps.
+struct AttendItem {
+  int v[12];
+};
+
+// A ring of items in shared memory: one warp fills it while the others are still busy with
+// earlier units, so that finding a unit (divisions, lengths in global memory) costs them nothing.
+struct ItemRing {
+  static constexpr int SLOTS = 4;
+  AttendItem item[SLOTS];
+  uint64_t full[SLOTS], empty[SLOTS];
+
+  __device__ __forceinline__ void init() {
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kItemReaders);
+    }
+  }
+  // By one thread.
+  __device__ __forceinline__ bool put(uint32_t i, const AttendItem& x, uint32_t* err, volatile int* abort_flag) {
+    const uint32_t s = i % SLOTS, r = i / SLOTS;
+    if (r > 0 && !mbar_wait(&empty[s], (r - 1) & 1, err, abort_flag)) return false;
+    item[s] = x;
+    mbar_arrive(&full[s]);
+    return true;
+  }
+  // By one thread, as one of kItemReaders.
+  __device__ __forceinline__ bool get_one(uint32_t i, AttendItem& x, uint32_t* err, volatile int* abort_flag) {
+    const uint32_t s = i % SLOTS, r = i / SLOTS;
+    if (!mbar_wait(&full[s], r & 1, err, abort_flag)) return false;
+    x = item[s];
+    mbar_arrive(&empty[s]);
+    return true;
+  }
+  // By a whole warp (one of kItemReaders); false: the wait ran out.
+  __device__ __forceinline__ bool get(uint32_t i, AttendItem& x, uint32_t* err, volatile int* abort_flag) {
+    const uint32_t s = i % SLOTS, r = i / SLOTS;
+    if (!warp_wait(&full[s], r & 1, err, abort_flag)) return false;
+    x = item[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
+    return true;
+  }
+};
+
+// Where a CTA begins a unit that others go on with: that unit, the last CTA with a part of it and
+// all steps, for the join.
+__device__ __forceinline__ void note_part(const AttendArgs& a, const AttendWork& w, int u, int lo, int hi, int n,
+                                          int to) {
+  if (lo != 0 || hi == n) return;
+  const int last = static_cast<int>(((w.end - to + n) * gridDim.x - 1) / w.total);  // holds the unit's last step
+  a.meta[blockIdx.x] = make_int4(u, last, static_cast<int>(w.total), 0);
+}
+
+// The slot of CTA c's part [lo, hi) of n, or -1 where it holds the whole unit.
+__device__ __forceinline__ int part_slot(int lo, int hi, int n) {
+  if (lo == 0 && hi == n) return -1;
+  return 2 * static_cast<int>(blockIdx.x) + (lo == 0 ? 1 : 0);
+}
+
+// With fewer steps than CTAs some ranges are empty, and their CTAs hold no part.
+__device__ __forceinline__ bool part_is_empty(int total, int C, int c) {
+  return static_cast<long long>(total) * c / C == static_cast<long long>(total) * (c + 1) / C;
+}
+
+
+// The MMA warp runs converged and every tcgen05 operation is predicated on its one issuing lane
+// (`lead`): operands stay in uniform registers, and issuing an MMA costs no branch. An MMA of 128
+// rows takes the tensor cores about 64 cycles, so that the issue, not the product, is the limit
+// where the operands are built anew for each.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  if (accumulate)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  if (accumulate)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(lead)
+        : "memory");
+}
+// Arrive on the mbarrier when every MMA issued so far is done.
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
+// A 128-byte-swizzle descriptor in two words: the low one holds the start address (in units of 16
+// bytes, so the steps of a product add constants) and the leading offset, the high one is a constant.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024 bytes between 8-row groups
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+// The same value in all lanes, as the compiler should know.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// D[128 x N] = A B^T over D channels, N = 128 rows of B or 64.
+template <int D, int N>
+__device__ __forceinline__ void issue_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
+  constexpr uint32_t id = idesc_bf16_f32(128, N, 0, 0);
+  const uint32_t ad = uniform(desc_lo(a_smem, 16)), bd = uniform(desc_lo(b_smem, 16));
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint64_t ad = smem_desc_sw128(a_smem + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024);
-    const uint64_t bd = smem_desc_sw128(b_smem + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024);
-    umma_bf16_ss(d_tmem, ad, bd, id, kk > 0 ? 1u : 0u);
+    const uint32_t step = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+    mma_ss(lead, d_tmem, desc_of(ad + step), desc_of(bd + step), id, kk > 0);
   }
 }
 
-// D[128 x D] (+)= P B over the tile's 128 rows. P's 16-row steps are 8 TMEM columns each;
-// HALF: the columns of rows 64.. start HALF columns behind those of rows 0.. (32: no gap).
-template <int D, int HALF>
-__device__ __forceinline__ void issue_ts(uint32_t d_tmem, uint32_t p_tmem, uint32_t b_smem, bool accumulate) {
+// D[128 x D] (+)= P B over the rows [16 K0, 16 K1) of the tile at b_smem. P's 16-row steps are 8 TMEM
+// columns each; the columns of rows 64.. start GAP columns behind those of rows 0..
+template <int D, int K0, int K1, int GAP>
+__device__ __forceinline__ void issue_ts(uint32_t lead, uint32_t d_tmem, uint32_t p_tmem, uint32_t b_smem,
+                                         bool accumulate) {
   constexpr uint32_t id = idesc_bf16_f32(128, D, 0, 1);
+  const uint32_t bd = uniform(desc_lo(b_smem, kBox));
+  if (accumulate)
+    mma_ts(lead, d_tmem, p_tmem + (K0 >> 2) * GAP + (K0 & 3) * 8, desc_of(bd + (K0 * 2048 >> 4)), id, true);
+  else
+    mma_ts(lead, d_tmem, p_tmem + (K0 >> 2) * GAP + (K0 & 3) * 8, desc_of(bd + (K0 * 2048 >> 4)), id, false);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint64_t bd = smem_desc_sw128(b_smem + kk * 2048, kBox, 1024);
-    umma_bf16_ts(d_tmem, p_tmem + (kk >> 2) * HALF + (kk & 3) * 8, bd, id, (accumulate || kk > 0) ? 1u : 0u);
-  }
+  for (int kk = K0 + 1; kk < K1; ++kk)
+    mma_ts(lead, d_tmem, p_tmem + (kk >> 2) * GAP + (kk & 3) * 8, desc_of(bd + (kk * 2048 >> 4)), id, true);
 }
+
+// A place in a ring of n stages: its index, and the parity of its current round.
+struct RingPos {
+  uint32_t s = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++s == n) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 // Rows [lo, hi) of a tile to zero, by a whole warp, before an MMA reads them: rows that no
 // query or key may see can hold anything, and 0 * NaN is not 0.
@@ -119,7 +373,7 @@ __device__ __forceinline__ void store_row32(float* p, const uint32_t (&x)[32], f
   }
 }
 
-// Where a kernel writes rows: bf16 with strides, or fp32 partial rows [split][row] of D.
+// Where a kernel writes whole rows.
 struct RowOut {
   __nv_bfloat16* p;
   long long sb, sh, sn;  // elements

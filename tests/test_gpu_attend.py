@@ -70,6 +70,10 @@ SHAPES = [
     (1, 2, 2, 1000, 1000),
     (3, 5, 1, 33, 2049),
     (1, 1, 1, 2500, 129),
+    (2, 10, 2, 13, 1500),   # nine heads of thirteen queries to a tile: five fit
+    (1, 24, 2, 11, 700),    # twelve heads of a group: eleven in one tile, one in the next
+    (1, 3, 3, 128, 777),    # the most queries of one tile
+    (40, 4, 2, 130, 130),   # more units than SMs
 ]
 
 
