@@ -81,6 +81,8 @@ _lib_lock = threading.Lock()
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libsla.so and declare its signatures. Raises if the library is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is not None:
             return _lib
@@ -541,7 +543,7 @@ def _check_heads(name, t, B, H, N, D, dtype, device):
     """A [B, H, N, D] tensor whose channels are contiguous (the library checks the other strides)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != (B, H, N, D) or (D > 1 and t.stride(3) != 1):
+    if t.dtype != dtype or t.shape != (B, H, N, D) or (D > 1 and t.stride(3) != 1):
         raise ValueError(f"{name} must be {dtype} of shape {(B, H, N, D)} with contiguous channels, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     if t.device != device:
@@ -552,7 +554,29 @@ def _tensor(t: Optional[torch.Tensor]):
     if t is None:
         return None
     s = t.stride()
-    return ctypes.byref(Tensor(t.data_ptr(), s[0], s[1], s[2]))
+    return Tensor(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _address(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+class _Call:
+    """Calls a library function with the device of its tensors current, on torch's current stream there. (Where
+    that device is current already, as it nearly always is, nothing is switched.)"""
+
+    def __init__(self, device):
+        self.device = device
+        self.stream = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __call__(self, f, *args):
+        if torch.cuda.current_device() == self.device.index:
+            status = f(*args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = f(*args, self.stream)
+        if status != SLA_OK:
+            _raise(status)
 
 
 def _span(t):
@@ -603,15 +627,13 @@ def _rotary_call(q, k, spec, out, dtype, names, backward):
             _check_in_place(f"out of {name}", x, y)
         heads.append(H)
         outs.append(y)
-    code = {torch.bfloat16: 0, torch.float32: 1}
-    lib = load_library()
-    args = (_tensor(q), _tensor(outs[0]), _tensor(k), _tensor(outs[1]), _stream_handle(dev))
-    with torch.cuda.device(dev):
-        if backward:
-            st = lib.sla_rotary_backward(ctypes.byref(spec), B, *heads, N, D, code[in_dtype], code[dtype], *args)
-        else:
-            st = lib.sla_rotary(ctypes.byref(spec), B, *heads, N, D, code[in_dtype], *args)
-    _raise(st)
+    lib, call = load_library(), _Call(dev)
+    args = (_tensor(q), _tensor(outs[0]), _tensor(k), _tensor(outs[1]))
+    in_code, out_code = int(in_dtype == torch.float32), int(dtype == torch.float32)  # SLA_BF16, SLA_F32
+    if backward:
+        call(lib.sla_rotary_backward, spec, B, heads[0], heads[1], N, D, in_code, out_code, *args)
+    else:
+        call(lib.sla_rotary, spec, B, heads[0], heads[1], N, D, in_code, *args)
     return outs[0], outs[1]
 
 
@@ -649,7 +671,7 @@ def new_workspace_attend(p: AttendProblem, device, backward: bool = False) -> to
 
 def _attend_space(p, device, backward):
     lib = load_library()
-    n = (lib.sla_workspace_size_attend_backward if backward else lib.sla_workspace_size_attend)(ctypes.byref(p))
+    n = (lib.sla_workspace_size_attend_backward if backward else lib.sla_workspace_size_attend)(p)
     if n == 0:
         raise SlaError(1, lib.sla_last_error().decode(errors="replace"))
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -683,11 +705,8 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
     lse = torch.empty(p.B, p.H, p.Nq, dtype=torch.float32, device=dev)
     if ws is None:
         ws = _attend_space(p, dev, False)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.sla_attend(ctypes.byref(p), _tensor(q), _tensor(k), _tensor(v), _ptr(kv_lens), _tensor(out), _ptr(lse),
-                            _ptr(ws), ctypes.c_size_t(ws.numel()), _stream_handle(dev))
-    _raise(st)
+    _Call(dev)(load_library().sla_attend, p, _tensor(q), _tensor(k), _tensor(v), _address(kv_lens), _tensor(out),
+               lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
 
 
@@ -704,12 +723,8 @@ def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=Non
     dk, dv = (torch.empty(p.B, p.Hk, p.Nk, p.D, dtype=torch.bfloat16, device=dev) for _ in range(2))
     if ws is None:
         ws = _attend_space(p, dev, True)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        st = lib.sla_attend_backward(ctypes.byref(p), _tensor(q), _tensor(k), _tensor(v), _tensor(out), _ptr(lse),
-                                     _tensor(dO), _ptr(kv_lens), _tensor(dq), _tensor(dk), _tensor(dv), _ptr(ws),
-                                     ctypes.c_size_t(ws.numel()), _stream_handle(dev))
-    _raise(st)
+    _Call(dev)(load_library().sla_attend_backward, p, _tensor(q), _tensor(k), _tensor(v), _tensor(out), lse.data_ptr(),
+               _tensor(dO), _address(kv_lens), _tensor(dq), _tensor(dk), _tensor(dv), ws.data_ptr(), ws.numel())
     return dq, dk, dv
 
 

@@ -513,47 +513,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the unit that CTA blockIdx.x of attend_kernel began and others went on
-// with: out = sum_p 2^(lse2_p - lse2) part_p in ascending CTA order, one warp per row.
+// with: out = sum_p 2^(lse2_p - lse2) part_p in ascending CTA order. 8 channels a thread.
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendFwdArgs f) {
+  constexpr int T = D / 8;
   const AttendArgs& a = f.p;
   grid_dep_wait();
   const int C = gridDim.x, c0 = blockIdx.x;
   const int4 meta = a.meta[c0];
   if (meta.x < 0) return;
   const int rows = f.narrow ? kTile : 2 * kTile;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = blockIdx.y * (256 / T) + threadIdx.x / T, c = (threadIdx.x % T) * 8;
   const AttendUnit w = attend_unit(f, meta.x, false);
   int h, i;
   if (!attend_row(f, w, row / kTile, row % kTile, h, i)) return;
-  constexpr int E = D / 32;
-  // Slots: 2 c0 + 1, then 2 c of every later CTA up to meta.y.
-  auto slot_row = [&](int c) { return static_cast<size_t>(c == c0 ? 2 * c + 1 : 2 * c) * rows + row; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= meta.y; c += 32)
-    if (!part_is_empty(meta.z, C, c)) m = fmaxf(m, f.part_lse2[slot_row(c)]);
+  // Slots: 2 c0 + 1, then 2 k of every later CTA k up to meta.y.
+  float m = -INFINITY, sum = 0.f, acc[8] = {};
+  for (int k = c0; k <= meta.y; ++k) {
+    if (part_is_empty(meta.z, C, k)) continue;
+    const size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k) * rows + row;
+    const float lse2 = f.part_lse2[at];
+    const float4* p = reinterpret_cast<const float4*>(f.part + at * D + c);
+    const float4 u = p[0], v = p[1];
+    const float top = fmaxf(m, lse2);
+    if (top == -INFINITY) continue;  // no part has seen a key yet
+    const float g = exp2f(m - top), e = exp2f(lse2 - top);
+    const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    sum = sum * g + e;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= meta.y; ++c) {
-    if (part_is_empty(meta.z, C, c)) continue;
-    const size_t at = slot_row(c);
-    const float g = exp2f(f.part_lse2[at] - ref);
-    sum += g;
-    const float* p = f.part + at * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(g, p[e], acc[e]);
+    for (int q = 0; q < 8; ++q) acc[q] = acc[q] * g + e * x[q];
+    m = top;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  __nv_bfloat16* out = f.out.p + w.b * f.out.sb + h * f.out.sh + i * f.out.sn + lane * E;
+  uint32_t o[4];
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(out + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0)
+  for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
+  *reinterpret_cast<uint4*>(f.out.p + w.b * f.out.sb + h * f.out.sh + i * f.out.sn + c) =
+      make_uint4(o[0], o[1], o[2], o[3]);
+  if (c == 0)
     f.lse[(static_cast<size_t>(w.b) * a.H + h) * a.Nq + i] =
         sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }

@@ -28,16 +28,21 @@ struct Share {
   bool cut;  // units may be cut into parts
 };
 
-// `units` units of at most `steps` steps each. Where whole units would leave CTAs idle (fewer
-// units than CTAs, a last wave that is mostly empty, or units of unlike length), the steps
-// behind the whole waves are cut into equal ranges, at least two steps to a range.
-// Units of like length: all waves but the last two go out whole. Many units of unlike length: over 64 to a
-// CTA their differences even out, and a scan over them would cost more than it saves.
+// `units` units of at most `steps` steps each. Whole units leave CTAs idle where there are fewer
+// units than CTAs, where the last wave is not full, or where units are of unlike length; then the
+// steps behind the whole waves are cut into equal ranges, at least two steps to a range.
+// Units of like length: all waves but the last two go out whole, and nothing is cut where that
+// saves less than kJoinCost steps, what joining the parts takes (17 us, against 8 us that cutting
+// the last of 11 waves of 4 steps saves). Many units of unlike length: over 64 to a CTA their
+// differences even out, and the scan over them would cost more than it saves.
+constexpr double kJoinCost = 8;
+
 Share share_out(long long units, long long steps, bool uniform) {
   Share s{static_cast<int>(units), 0, 0, uniform ? 1 : 0, false};
-  const long long waves = (units + kSms - 1) / kSms;
-  const bool even = uniform && units * 100 >= waves * kSms * 95;
-  if (even || units > 64ll * kSms || units * (steps + sla::kUnitCost) >= (1ll << 31)) {
+  const long long waves = (units + kSms - 1) / kSms, unit = steps + sla::kUnitCost;
+  const double saved = static_cast<double>(unit) * (waves - static_cast<double>(units) / kSms);
+  const bool short_tail = waves >= 4 && unit < kJoinCost;  // of unlike length: at most about one unit is lost
+  if ((uniform && saved < kJoinCost) || short_tail || units > 64ll * kSms || units * unit >= (1ll << 31)) {
     s.ctas = static_cast<int>(units < kSms ? units : kSms);
     s.waves = static_cast<int>(waves);
     return s;
@@ -223,7 +228,7 @@ sla_status launch_forward(const AttendPlan& w, const Maps& m, const AttendFwdArg
   SLA_TRY(launch_dependent(sla::attend_kernel<D>, dim3(w.fwd.ctas), dim3(sla::kThreads), smem, st, "attend_kernel", m.q, m.k,
                            m.v, f));
   if (w.fwd.cut)
-    SLA_TRY(launch_dependent(sla::attend_join_kernel<D>, dim3(w.fwd.ctas, (w.narrow ? 1 : 2) * kTile / 8), dim3(256), 0,
+    SLA_TRY(launch_dependent(sla::attend_join_kernel<D>, dim3(w.fwd.ctas, (w.narrow ? 1 : 2) * kTile / (256 / (D / 8))), dim3(256), 0,
                              st, "attend_join_kernel", f));
   return SLA_OK;
 }
@@ -232,8 +237,8 @@ template <int D>
 sla_status launch_backward(const AttendPlan& w, const Maps& m, const AttendRowsArgs& r, const AttendBwdArgs& kv,
                            const AttendBwdArgs& q, cudaStream_t st) {
   constexpr int per = 256 / (D / 8);
-  SLA_TRY(launch_dependent(sla::attend_rows_kernel<D>, dim3(static_cast<unsigned>((r.rows + per - 1) / per)), dim3(256),
-                           0, st, "attend_rows_kernel", r));
+  const unsigned blocks = static_cast<unsigned>(w.p.B) * w.p.H * (w.pad / (per * sla::kRowsUnroll));
+  SLA_TRY(launch_dependent(sla::attend_rows_kernel<D>, dim3(blocks), dim3(256), 0, st, "attend_rows_kernel", r));
   constexpr int smem_kv = sla::AttendDkvSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dkv_kernel<D>, smem_kv));
   SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kThreads), smem_kv, st, "attend_dkv_kernel",
@@ -323,7 +328,7 @@ sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q,
   SLA_TRY(operand_map(&m.v, v, p->B, p->Hk, p->Nk, p->D));
   SLA_TRY(operand_map(&m.g, dO, p->B, p->H, p->Nq, p->D));
   const RowOut o = row_out(out, p->B, p->H, p->Nq), g = row_out(dO, p->B, p->H, p->Nq);
-  const AttendRowsArgs r{p->H, p->Nq, w.pad, static_cast<long long>(p->B) * p->H * w.pad,
+  const AttendRowsArgs r{p->H, p->Nq, w.pad,
                          o.p,  g.p,   o.sb,  o.sh, o.sn, g.sb, g.sh, g.sn, lse, s.nlse, s.ndelta};
   AttendBwdArgs f{};
   f.p = common_args(w, kv_lens, s.err, w.dkv, s.meta);

@@ -29,46 +29,62 @@ struct AttendBwdArgs {
   float* part;          // parts of units (see AttendWork): dQ [2 * CTAs][128][D], or [2 * CTAs][dK, dV][128][D]
 };
 
-// -lse2 and -delta of every row, 8 channels a lane. Reads out and dO once (bound by HBM).
+// -lse2 and -delta of every row, 8 channels a lane, kRowsUnroll rows a thread so that their loads
+// are in flight together. Reads out and dO once (bound by HBM).
 struct AttendRowsArgs {
   int H, Nq, pad;
-  long long rows;  // B * H * pad
   const __nv_bfloat16 *out, *dO;
   long long ob, oh, on, gb, gh, gn;
   const float* lse;
   float *nlse, *ndelta;
 };
 
+constexpr int kRowsUnroll = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) attend_rows_kernel(AttendRowsArgs a) {
-  constexpr int T = D / 8;  // lanes of a row, 8 channels each
-  const long long i = static_cast<long long>(blockIdx.x) * (256 / T) + threadIdx.x / T;
+  constexpr int T = D / 8, U = kRowsUnroll;  // lanes of a row
+  // A block's rows are of one head (pad is a multiple of 128).
+  const int per_head = a.pad / (256 / T * U), bh = blockIdx.x / per_head;
+  const int row0 = blockIdx.x % per_head * (256 / T * U) + threadIdx.x / T;
   const int c = (threadIdx.x % T) * 8;
   grid_dep_wait();
-  const int row = static_cast<int>(i % a.pad);
-  const long long bh = i / a.pad;
-  float nl = -INFINITY, sum = 0.f;
-  if (i < a.rows && row < a.Nq) {
-    nl = -a.lse[bh * a.Nq + row] * 1.4426950408889634f;
-    const long long b = bh / a.H, h = bh % a.H;
-    if (nl == INFINITY) {  // a row without keys
-      nl = -INFINITY;
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(a.out + b * a.ob + h * a.oh + row * a.on + c);
-      const uint4 y = *reinterpret_cast<const uint4*>(a.dO + b * a.gb + h * a.gh + row * a.gn + c);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const int b = bh / a.H, h = bh % a.H;
+  const __nv_bfloat16* const out = a.out + b * a.ob + h * a.oh + c;
+  const __nv_bfloat16* const dO = a.dO + b * a.gb + h * a.gh + c;
+  uint4 x[U], y[U];
+  float nl[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 u = unpack_bf16x2(xs[k]), v = unpack_bf16x2(ys[k]);
-        sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
-      }
+  for (int u = 0; u < U; ++u) {
+    const int row = row0 + u * (256 / T);
+    x[u] = y[u] = make_uint4(0, 0, 0, 0);
+    nl[u] = -INFINITY;
+    if (row < a.Nq) {
+      nl[u] = -a.lse[static_cast<size_t>(bh) * a.Nq + row] * 1.4426950408889634f;
+      x[u] = *reinterpret_cast<const uint4*>(out + row * a.on);
+      y[u] = *reinterpret_cast<const uint4*>(dO + row * a.gn);
     }
   }
 #pragma unroll
-  for (int o = T / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (c == 0 && i < a.rows) {
-    a.nlse[i] = nl;
-    a.ndelta[i] = -sum;
+  for (int u = 0; u < U; ++u) {
+    float sum = 0.f;
+    if (nl[u] == INFINITY) {  // a row without keys: its dO may hold anything
+      nl[u] = -INFINITY;
+    } else {
+      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 p = unpack_bf16x2(xs[k]), q = unpack_bf16x2(ys[k]);
+        sum = fmaf(p.x, q.x, fmaf(p.y, q.y, sum));
+      }
+    }
+#pragma unroll
+    for (int o = T / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (c == 0) {
+      const size_t i = static_cast<size_t>(bh) * a.pad + row0 + u * (256 / T);
+      a.nlse[i] = nl[u];
+      a.ndelta[i] = -sum;
+    }
   }
 }
 
@@ -131,6 +147,76 @@ struct DkvItem {
   __device__ __forceinline__ bool stop() const { return b < 0; }
 };
 
+template <int ST>
+struct DkvBarriers {
+  uint64_t kv_full, kv_free, s_full, dp_full, p_full, t_full, acc_full[2], acc_free[2], drain;  // [dV, dK]
+  uint64_t q_full[ST], g_full[ST], q_free[ST], g_free[ST];
+  int abort_flag;
+};
+
+// One of the two MMA warps. Y = 0: S^T(i) = K Q_i^T, then dV += P(i)^T dO_i. Y = 1: dP^T(i) = V dO_i^T, then
+// dK += T(i)^T Q_i. Each chain's own order keeps S^T(i + 1) from overwriting P(i), and dP^T(i + 1) T(i).
+// What a product needs besides P or T is looked up before P or T is waited for.
+template <int D, int Y>
+__device__ __forceinline__ void attend_dkv_issue(DkvBarriers<AttendDkvSmem<D>::STAGES>& sh, ItemRing& items,
+                                                 const AttendBwdArgs& f, uint8_t* kv, uint8_t* ring) {
+  using L = AttendDkvSmem<D>;
+  constexpr int ST = L::STAGES;
+  constexpr uint32_t col = Y ? 128 : 0, acc = Y ? 384 : 256;          // TMEM columns of the products
+  constexpr uint32_t one = Y ? L::TILE : 0, two = Y ? 0 : L::TILE;    // their tiles in a stage
+  uint64_t *const full1 = Y ? sh.g_full : sh.q_full, *const free1 = Y ? sh.g_free : sh.q_free;
+  uint64_t *const full2 = Y ? sh.q_full : sh.g_full, *const free2 = Y ? sh.q_free : sh.g_free;
+  uint64_t *const made = Y ? &sh.dp_full : &sh.s_full, *const formed = Y ? &sh.t_full : &sh.p_full;
+  const uint32_t a0 = smem_u32(kv), r0 = smem_u32(ring);
+  uint32_t nu = 0, ni = 0, done = 0;  // units with work, items, parity of the next P or T
+  RingPos pos;                        // of the first product's tile
+  bool ok = true;
+  AttendItem item;
+  const uint32_t lead = elect_one();
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, f.p.err, &sh.abort_flag); };
+  auto issue_first = [&](bool last) {
+    issue_ss<D, 128>(lead, col, a0, r0 + pos.s * L::STAGE + one);
+    mma_commit(lead, made);
+    mma_commit(lead, &free1[pos.s]);
+    if (last) mma_commit(lead, &sh.kv_free);  // the unit's last reader of K_j or V_j
+    pos.next(ST);
+  };
+  while (ok) {
+    if (!(ok = items.get(ni++, item, f.p.err, &sh.abort_flag))) break;
+    const DkvItem w(item);
+    if (w.stop()) break;
+    const int n = w.n;
+    if (n == 0) continue;
+    if (!(ok = wait(&sh.kv_full, nu & 1))) break;
+    RingPos cur = pos;  // of the second product's tile
+    if (!(ok = wait(&full1[pos.s], pos.parity))) break;
+    tc_fence_after();
+    issue_first(n == 1);
+    if (nu > 0 && !(ok = wait(&sh.acc_free[Y], (nu - 1) & 1))) break;
+    int i_tile = w.lo % w.tiles;
+    for (int i = 0; i < n; ++i) {
+      uint8_t* tile = ring + cur.s * L::STAGE + two;
+      if (!(ok = wait(&full2[cur.s], cur.parity))) break;
+      // Rows that see no key may hold anything: zero them where the product sums over rows.
+      const int row = (w.first + i_tile) * kTile;
+      if (row < w.dead) zero_rows<D>(tile, 0, min(kTile, w.dead - row));
+      if (++i_tile == w.tiles) i_tile = 0;
+      if (i + 1 < n && !(ok = wait(&full1[pos.s], pos.parity))) break;
+      if (!(ok = wait(formed, done))) break;
+      done ^= 1;
+      tc_fence_after();
+      issue_ts<D, 0, 8, 64>(lead, acc, col, smem_u32(tile), i > 0);
+      mma_commit(lead, &free2[cur.s]);
+      if (i + 1 == n) mma_commit(lead, &sh.acc_full[Y]);
+      cur.next(ST);
+      if (i + 1 < n) issue_first(i + 2 == n);
+    }
+    ++nu;
+  }
+  mma_commit(lead, &sh.drain);
+  mbar_wait(&sh.drain, 0, nullptr, nullptr);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -147,33 +233,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = sV + L::TILE;                                           // Q then dO
   float* stats = reinterpret_cast<float*>(ring + ST * L::STAGE);          // nlse[128] then ndelta[128]
 
-  __shared__ uint64_t kv_full, kv_free, s_full, dp_full, p_full, t_full, acc_full[2], acc_free[2], drain;  // [dV, dK]
-  __shared__ uint64_t q_full[ST], g_full[ST], q_free[ST], g_free[ST];
+  __shared__ DkvBarriers<ST> sh;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag;
   __shared__ ItemRing items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(&kv_full, 1);
-    mbar_init(&kv_free, 2);
-    mbar_init(&s_full, 1);
-    mbar_init(&dp_full, 1);
-    mbar_init(&p_full, 256);
-    mbar_init(&t_full, 256);
-    mbar_init(&acc_full[0], 1);
-    mbar_init(&acc_full[1], 1);
-    mbar_init(&acc_free[0], 128);
-    mbar_init(&acc_free[1], 128);
-    mbar_init(&drain, 2);
+    mbar_init(&sh.kv_full, 1);
+    mbar_init(&sh.kv_free, 2);
+    mbar_init(&sh.s_full, 1);
+    mbar_init(&sh.dp_full, 1);
+    mbar_init(&sh.p_full, 8);
+    mbar_init(&sh.t_full, 8);
+    mbar_init(&sh.acc_full[0], 1);
+    mbar_init(&sh.acc_full[1], 1);
+    mbar_init(&sh.acc_free[0], 128);
+    mbar_init(&sh.acc_free[1], 128);
+    mbar_init(&sh.drain, 2);
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&g_full[s], 1);
-      mbar_init(&q_free[s], 2);
-      mbar_init(&g_free[s], 2);
+      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.g_full[s], 1);
+      mbar_init(&sh.q_free[s], 2);
+      mbar_init(&sh.g_free[s], 2);
     }
     items.init();
-    abort_flag = 0;
+    sh.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -198,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         note_part(a, work, u, lo, hi, n, to);
         const DkvUnit w = dkv_unit(a, u, true);
         item = {w.b, w.hk, w.key0, w.len, w.first, w.tiles, w.dead, lo, hi, part_slot(lo, hi, n)};
-        ok = items.put(ni++, item, a.err, &abort_flag);
+        ok = items.put(ni++, item, a.err, &sh.abort_flag);
       }
       item.v[0] = -1;
-      if (ok) items.put(ni, item, a.err, &abort_flag);
+      if (ok) items.put(ni, item, a.err, &sh.abort_flag);
     }
     __syncwarp();
   } else if (warp == kProducerWarp) {
@@ -215,95 +299,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t nr = 0, nu = 0, ng = 0;  // Q tiles, units and dO tiles loaded
       bool ok = true;
       while (ok) {
-        if (!(ok = items.get_one(ni++, item, a.err, &abort_flag))) break;
+        if (!(ok = items.get_one(ni++, item, a.err, &sh.abort_flag))) break;
         const DkvItem w(item);
         if (w.stop()) break;
         if (w.n == 0) continue;
-        if (nu > 0 && !(ok = mbar_wait(&kv_free, (nu - 1) & 1, a.err, &abort_flag))) break;
-        mbar_arrive_expect_tx(&kv_full, 2 * L::TILE);
-        for (int b = 0; b < DB; ++b) tma_load_4d(sK + b * kBox, &map_k, &kv_full, b * 64, w.key0, w.hk, w.b);
-        for (int b = 0; b < DB; ++b) tma_load_4d(sV + b * kBox, &map_v, &kv_full, b * 64, w.key0, w.hk, w.b);
+        if (nu > 0 && !(ok = mbar_wait(&sh.kv_free, (nu - 1) & 1, a.err, &sh.abort_flag))) break;
+        mbar_arrive_expect_tx(&sh.kv_full, 2 * L::TILE);
+        for (int b = 0; b < DB; ++b) tma_load_4d(sK + b * kBox, &map_k, &sh.kv_full, b * 64, w.key0, w.hk, w.b);
+        for (int b = 0; b < DB; ++b) tma_load_4d(sV + b * kBox, &map_v, &sh.kv_full, b * 64, w.key0, w.hk, w.b);
         ++nu;
         for (int i = w.lo; i < w.lo + w.n; ++i) {
           const int h = w.hk * a.G + i / w.tiles, row = (w.first + i % w.tiles) * kTile;
           const uint32_t s = nr % ST, r = nr / ST;
-          if (r > 0 && !(ok = mbar_wait(&q_free[s], (r - 1) & 1, a.err, &abort_flag))) break;
+          if (r > 0 && !(ok = mbar_wait(&sh.q_free[s], (r - 1) & 1, a.err, &sh.abort_flag))) break;
           const size_t at = (static_cast<size_t>(w.b) * a.H + h) * f.pad + row;
           uint8_t* stage = ring + s * L::STAGE;
           float* st = stats + s * 2 * kTile;
-          mbar_arrive_expect_tx(&q_full[s], L::TILE + L::STATS);
-          for (int b = 0; b < DB; ++b) tma_load_4d(stage + b * kBox, &map_q, &q_full[s], b * 64, row, h, w.b);
-          bulk_load(st, f.nlse + at, &q_full[s], kTile * 4);
-          bulk_load(st + kTile, f.ndelta + at, &q_full[s], kTile * 4);
+          mbar_arrive_expect_tx(&sh.q_full[s], L::TILE + L::STATS);
+          for (int b = 0; b < DB; ++b) tma_load_4d(stage + b * kBox, &map_q, &sh.q_full[s], b * 64, row, h, w.b);
+          bulk_load(st, f.nlse + at, &sh.q_full[s], kTile * 4);
+          bulk_load(st + kTile, f.ndelta + at, &sh.q_full[s], kTile * 4);
           ++nr;
-          if (r > 0 && !(ok = mbar_wait(&g_free[s], (r - 1) & 1, a.err, &abort_flag))) break;
-          mbar_arrive_expect_tx(&g_full[s], L::TILE);
+          if (r > 0 && !(ok = mbar_wait(&sh.g_free[s], (r - 1) & 1, a.err, &sh.abort_flag))) break;
+          mbar_arrive_expect_tx(&sh.g_full[s], L::TILE);
           for (int b = 0; b < DB; ++b)
-            tma_load_4d(stage + L::TILE + b * kBox, &map_g, &g_full[s], b * 64, row, h, w.b);
+            tma_load_4d(stage + L::TILE + b * kBox, &map_g, &sh.g_full[s], b * 64, row, h, w.b);
           ++ng;
         }
       }
-      if (abort_flag) {  // let every load still in flight land before the CTA retires
-        if (nu > 0) mbar_wait(&kv_full, (nu - 1) & 1, nullptr, nullptr);
-        for (uint32_t i = nr > ST ? nr - ST : 0; i < nr; ++i) mbar_wait(&q_full[i % ST], (i / ST) & 1, nullptr, nullptr);
-        for (uint32_t i = ng > ST ? ng - ST : 0; i < ng; ++i) mbar_wait(&g_full[i % ST], (i / ST) & 1, nullptr, nullptr);
+      if (sh.abort_flag) {  // let every load still in flight land before the CTA retires
+        if (nu > 0) mbar_wait(&sh.kv_full, (nu - 1) & 1, nullptr, nullptr);
+        for (uint32_t i = nr > ST ? nr - ST : 0; i < nr; ++i) mbar_wait(&sh.q_full[i % ST], (i / ST) & 1, nullptr, nullptr);
+        for (uint32_t i = ng > ST ? ng - ST : 0; i < ng; ++i) mbar_wait(&sh.g_full[i % ST], (i / ST) & 1, nullptr, nullptr);
       }
     }
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     // ------------------------------------------------------------ MMA issuers
-    // The first warp: S^T(i) = K Q_i^T, then dV += P(i)^T dO_i. The second: dP^T(i) = V dO_i^T, then dK +=
-    // T(i)^T Q_i. Each chain's own order keeps S^T(i + 1) from overwriting P(i), and dP^T(i + 1) T(i).
-    const int y = warp == kMmaWarp2;
-    const uint32_t a0 = smem_u32(y ? sV : sK), r0 = smem_u32(ring);
-    const uint32_t col = y ? TP : 0, acc = y ? TK : TV;  // TMEM columns of the products
-    const uint32_t one = y ? L::TILE : 0, two = y ? 0 : L::TILE;  // first and second product's tile in a stage
-    uint32_t nu = 0, ni = 0;
-    RingPos pos;           // of the first product's tile
-    uint32_t done = 0;     // parity of the next P or T
-    bool ok = true;
-    const uint32_t lead = elect_one();
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
-    auto issue_first = [&](bool last) -> bool {
-      const uint32_t s = pos.s;
-      if (!wait(y ? &g_full[s] : &q_full[s], pos.parity)) return false;
-      tc_fence_after();
-      issue_ss<D, 128>(lead, col, a0, r0 + s * L::STAGE + one);
-      mma_commit(lead, y ? &dp_full : &s_full);
-      mma_commit(lead, y ? &g_free[s] : &q_free[s]);
-      if (last) mma_commit(lead, &kv_free);  // the unit's last reader of K_j or V_j
-      pos.next(ST);
-      return true;
-    };
-    while (ok) {
-      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
-      const DkvItem w(item);
-      if (w.stop()) break;
-      const int n = w.n;
-      if (n == 0) continue;
-      if (!(ok = wait(&kv_full, nu & 1))) break;
-      RingPos cur = pos;  // of the second product's tile
-      if (!(ok = issue_first(n == 1))) break;
-      if (nu > 0 && !(ok = wait(&acc_free[y], (nu - 1) & 1))) break;
-      for (int i = 0; i < n; ++i) {
-        if (!(ok = wait(y ? &t_full : &p_full, done))) break;
-        done ^= 1;
-        uint8_t* tile = ring + cur.s * L::STAGE + two;
-        if (!(ok = wait(y ? &q_full[cur.s] : &g_full[cur.s], cur.parity))) break;
-        // Rows that see no key may hold anything: zero them where the product sums over rows.
-        const int row = (w.first + (w.lo + i) % w.tiles) * kTile;
-        if (row < w.dead) zero_rows<D>(tile, 0, min(kTile, w.dead - row));
-        tc_fence_after();
-        issue_ts<D, 0, 8, 64>(lead, acc, col, smem_u32(tile), i > 0);
-        mma_commit(lead, y ? &q_free[cur.s] : &g_free[cur.s]);
-        if (i + 1 == n) mma_commit(lead, &acc_full[y]);
-        cur.next(ST);
-        if (i + 1 < n && !(ok = issue_first(i + 2 == n))) break;
-      }
-      ++nu;
-    }
-    mma_commit(lead, &drain);
-    mbar_wait(&drain, 0, nullptr, nullptr);
+    if (warp == kMmaWarp)
+      attend_dkv_issue<D, 0>(sh, items, f, sK, ring);
+    else
+      attend_dkv_issue<D, 1>(sh, items, f, sV, ring);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ P and T, then the epilogue
     regs_up<kComputeRegs>();
@@ -316,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, nu = 0, ni = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return warp_wait(bar, parity, a.err, &abort_flag);
+      return warp_wait(bar, parity, a.err, &sh.abort_flag);
     };
     while (ok) {
-      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
+      if (!(ok = items.get(ni++, item, a.err, &sh.abort_flag))) break;
       const DkvItem w(item);
       if (w.stop()) break;
       const int n = w.n;
@@ -330,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // First column of this half whose query sees the key, 64: none. Queries from it on all do.
         const int from = key >= w.len ? 64 : a.causal ? max(0, key - (w.len - a.Nq) - row) : 0;
         const bool masked = __any_sync(0xffffffffu, from > 0);
-        if (!(ok = wait(&s_full, it & 1))) break;
-        if (!(ok = wait(&q_full[it % ST], (it / ST) & 1))) break;  // the rows' statistics
+        if (!(ok = wait(&sh.s_full, it & 1))) break;
+        if (!(ok = wait(&sh.q_full[it % ST], (it / ST) & 1))) break;  // the rows' statistics
         tc_fence_after();
         uint32_t p[2][32];
 #pragma unroll
@@ -358,8 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(s_addr, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full);
-        if (!(ok = wait(&dp_full, it & 1))) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full);
+        if (!(ok = wait(&sh.dp_full, it & 1))) break;
         tc_fence_after();
         uint32_t d[2][32];
 #pragma unroll
@@ -384,12 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(p_addr, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&t_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.t_full);
       }
       if (!ok) break;
       // Warps 4..7 write dV, warps 8..11 dK (times scale); zeros where no query saw the keys.
       if (n > 0) {
-        if (!(ok = wait(&acc_full[half], nu & 1))) break;
+        if (!(ok = wait(&sh.acc_full[half], nu & 1))) break;
         tc_fence_after();
       }
       const RowOut& o = half ? f.dk : f.dv;
@@ -417,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n > 0) {
         tc_fence_before();
-        mbar_arrive(&acc_free[half]);
+        mbar_arrive(&sh.acc_free[half]);
         ++nu;
       }
     }

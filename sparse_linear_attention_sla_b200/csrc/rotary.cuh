@@ -116,47 +116,81 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
   const int h1 = min(h0 + a.heads_per_block, a.heads[0] + a.heads[1]);
   const bool in = n < a.N;
 
+  // The block's frequencies, one for each pair of channels, then this thread's angles. Pairs of
+  // neighbours lie in one thread; halves share theirs through the table of all tokens' pairs.
+  __shared__ double freq[D / 2];
+  __shared__ float2 table[HALVES ? TOKENS * (D / 2) : 1];
+  const int turned_channels = a.first[a.n_axes];
+  auto axis_of = [&](int c) {
+    int ax = 0;
+    while (c >= a.first[ax + 1]) ++ax;
+    return ax;
+  };
+  if (threadIdx.x < D / 2 && 2 * threadIdx.x < turned_channels) {
+    const int ax = axis_of(2 * threadIdx.x), d = a.first[ax + 1] - a.first[ax];
+    freq[threadIdx.x] = exp2(-static_cast<double>(2 * threadIdx.x - a.first[ax]) / d * a.log2_base);
+  }
+  __syncthreads();
+  const bool turns = in && (a.pos || n < a.n_turned);
+  // cos and sin of pair p (counted over all axes) at token n: the angle in fp64, brought into
+  // [-pi, pi] with 2 pi as a sum of two doubles.
+  auto angle = [&](int p, int ax, float& co, float& s) {
+    int at;
+    if (a.pos) {
+      at = a.pos[b * a.pos_b + static_cast<long long>(n) * a.n_axes + ax];
+    } else {
+      int q = n;
+      for (int x = a.n_axes - 1; x > ax; --x) q /= a.grid[x];
+      at = q % a.grid[ax] + a.start[ax];
+    }
+    const double phi = at * freq[p];
+    const double full = rint(phi * 0.15915494309189535);
+    sincosf(static_cast<float>(fma(-full, 2.4492935982947064e-16, fma(-full, 6.283185307179586, phi))), &s, &co);
+    s *= a.sign;
+  };
+
   float cs[8], sn[8];   // y = x cs + partner sn
   int partner[8];       // HALVES: the partner's channel
   uint32_t turned = 0;  // channels that turn
 #pragma unroll
   for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f, partner[e] = c0 + e;
-  if (in && (a.pos || n < a.n_turned)) {
+  if constexpr (HALVES) {
+    if (turns) {
 #pragma unroll
-    for (int e = 0; e < 8; e += (HALVES ? 1 : 2)) {
-      const int c = c0 + e;
-      if (c >= a.first[a.n_axes]) continue;
-      int ax = 0;
-      while (c >= a.first[ax + 1]) ++ax;
-      const int d = a.first[ax + 1] - a.first[ax], half = d >> 1;
-      const int l = c - a.first[ax];
-      const int i = HALVES ? (l < half ? l : l - half) : l >> 1;
-      int p;
-      if (a.pos) {
-        p = a.pos[b * a.pos_b + static_cast<long long>(n) * a.n_axes + ax];
-      } else {
-        int q = n;
-        for (int x = a.n_axes - 1; x > ax; --x) q /= a.grid[x];
-        p = q % a.grid[ax] + a.start[ax];
+      for (int e = 0; e < 4; ++e) {
+        const int p = c0 / 2 + e;
+        if (2 * p >= turned_channels) continue;
+        float co, s;
+        angle(p, axis_of(2 * p), co, s);
+        table[(threadIdx.x / T) * (D / 2) + p] = make_float2(co, s);
       }
-      // The angle in fp64, brought into [-pi, pi] with 2 pi as a sum of two doubles.
-      const double phi = static_cast<double>(p) * exp2(-2.0 * i / d * a.log2_base);
-      const double turns = rint(phi * 0.15915494309189535);
-      const double r = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, phi));
-      float s, co;
-      sincosf(static_cast<float>(r), &s, &co);
-      s *= a.sign;
-      if (HALVES) {
-        cs[e] = co;
-        sn[e] = l < half ? -s : s;
-        partner[e] = a.first[ax] + (l < half ? l + half : l - half);
+    }
+    __syncwarp();  // a row's threads are of one warp
+    if (turns) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = c0 + e;
+        if (c >= turned_channels) continue;
+        const int ax = axis_of(c), half = (a.first[ax + 1] - a.first[ax]) >> 1, l = c - a.first[ax];
+        const bool lower = l < half;
+        const float2 t = table[(threadIdx.x / T) * (D / 2) + (a.first[ax] >> 1) + (lower ? l : l - half)];
+        cs[e] = t.x;
+        sn[e] = lower ? -t.y : t.y;
+        partner[e] = lower ? c + half : c - half;
         turned |= 1u << e;
-      } else {
-        cs[e] = cs[e + 1] = co;
-        sn[e] = -s;
-        sn[e + 1] = s;
-        turned |= 3u << e;
       }
+    }
+  } else if (turns) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int p = (c0 + e) / 2;
+      if (2 * p >= turned_channels) continue;
+      float co, s;
+      angle(p, axis_of(2 * p), co, s);
+      cs[e] = cs[e + 1] = co;
+      sn[e] = -s;
+      sn[e + 1] = s;
+      turned |= 3u << e;
     }
   }
 
