@@ -93,6 +93,20 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t* x) {
   return static_cast<uint64_t>(x[0]) | (static_cast<uint64_t>(x[1]) << 32);
 }
 
+// Of columns OFF .. OFF + 31 those before `from` (or, keep_upto, from `upto` on) take `value`.
+template <int OFF>
+__device__ __forceinline__ void keep_from(uint32_t (&x)[32], int from, float value) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (OFF + c < from) x[c] = __float_as_uint(value);
+}
+template <int OFF>
+__device__ __forceinline__ void keep_upto(uint32_t (&x)[32], int upto, float value) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (OFF + c >= upto) x[c] = __float_as_uint(value);
+}
+
 // ---------------------------------------------------------------------------- dK, dV
 
 // One persistent CTA per SM, 384 threads, on units of 128 keys of one key head, a step being a
@@ -373,6 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 32 * c, p[c]);
         tmem_wait_ld();
+        if (masked) {
+          keep_from<0>(p[0], from, -INFINITY);
+          keep_from<32>(p[1], from, -INFINITY);
+        }
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -380,11 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(st + 32 * c + e);
             const uint64_t x0 = f2_fma(pair_of(&p[c][e]), sc2, nl.x), x1 = f2_fma(pair_of(&p[c][e + 2]), sc2, nl.y);
-            float v[4] = {fast_exp2(f2_lo(x0)), fast_exp2(f2_hi(x0)), fast_exp2(f2_lo(x1)), fast_exp2(f2_hi(x1))};
-            if (masked) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = 32 * c + e + q >= from ? v[q] : 0.f;
-            }
+            const float v[4] = {fast_exp2(f2_lo(x0)), fast_exp2(f2_hi(x0)), fast_exp2(f2_lo(x1)), fast_exp2(f2_hi(x1))};
 #pragma unroll
             for (int q = 0; q < 4; ++q) p[c][e + q] = __float_as_uint(v[q]);
             pk[16 * c + e / 2] = pack_bf16x2(v[0], v[1]);
@@ -402,20 +416,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld32(p_addr + 32 * c, d[c]);
         tmem_wait_ld();
+        if (masked) {  // dP of a key that is not there may be NaN
+          keep_from<0>(d[0], from, 0.f);
+          keep_from<32>(d[1], from, 0.f);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(st + kTile + 32 * c + e);
-            uint64_t y0 = f2_mul(f2_add(pair_of(&d[c][e]), nd.x), pair_of(&p[c][e]));
-            uint64_t y1 = f2_mul(f2_add(pair_of(&d[c][e + 2]), nd.y), pair_of(&p[c][e + 2]));
-            float v[4] = {f2_lo(y0), f2_hi(y0), f2_lo(y1), f2_hi(y1)};
-            if (masked) {  // dP of a key that is not there may be NaN
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = 32 * c + e + q >= from ? v[q] : 0.f;
-            }
-            pk[16 * c + e / 2] = pack_bf16x2(v[0], v[1]);
-            pk[16 * c + e / 2 + 1] = pack_bf16x2(v[2], v[3]);
+            const uint64_t y0 = f2_mul(f2_add(pair_of(&d[c][e]), nd.x), pair_of(&p[c][e]));
+            const uint64_t y1 = f2_mul(f2_add(pair_of(&d[c][e + 2]), nd.y), pair_of(&p[c][e + 2]));
+            pk[16 * c + e / 2] = pack_bf16x2(f2_lo(y0), f2_hi(y0));
+            pk[16 * c + e / 2 + 1] = pack_bf16x2(f2_lo(y1), f2_hi(y1));
           }
         }
         tmem_st32(p_addr, pk);
@@ -733,6 +746,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 32 * c, p[c]);
         tmem_wait_ld();
+        if (masked) {
+          keep_upto<0>(p[0], upto, -INFINITY);
+          keep_upto<32>(p[1], upto, -INFINITY);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -749,18 +766,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(&dp_free);
+        if (masked) {  // dP of a key that is not there may be NaN
+          keep_upto<0>(d[0], upto, 0.f);
+          keep_upto<32>(d[1], upto, 0.f);
+        }
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const uint64_t y = f2_mul(f2_add(pair_of(&d[c][e]), nd2), pair_of(&p[c][e]));
-            float v[2] = {f2_lo(y), f2_hi(y)};
-            if (masked) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) v[q] = 32 * c + e + q < upto ? v[q] : 0.f;
-            }
-            pk[16 * c + e / 2] = pack_bf16x2(v[0], v[1]);
+            pk[16 * c + e / 2] = pack_bf16x2(f2_lo(y), f2_hi(y));
           }
         }
         tmem_st32(s_addr, pk);
