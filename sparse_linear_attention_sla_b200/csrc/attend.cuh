@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ST = f.narrow ? (L::STAGES + 1) / 2 : L::STAGES;
   const AttendArgs& a = f.p;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = base;
   uint8_t* ring = sQ + (2 - f.narrow) * L::TILE;
 

@@ -93,6 +93,13 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t* x) {
   return static_cast<uint64_t>(x[0]) | (static_cast<uint64_t>(x[1]) << 32);
 }
 
+// Two pairs from shared memory, as a shared load (a generic one waits in the queue of global accesses).
+__device__ __forceinline__ ulonglong2 load_shared16(uint32_t addr) {
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr));
+  return v;
+}
+
 // Of columns OFF .. OFF + 31 those before `from` (or, keep_upto, from `upto` on) take `value`.
 template <int OFF>
 __device__ __forceinline__ void keep_from(uint32_t (&x)[32], int from, float value) {
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t TP = 128, TV = 256, TK = 384;  // TMEM columns of dP^T, dV, dK
   const AttendArgs& a = f.p;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sK = base;
   uint8_t* sV = sK + L::TILE;
   uint8_t* ring = sV + L::TILE;                                           // Q then dO
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = w.key0 + r;
       for (int i = 0; i < n; ++i, ++it) {
         const int row = (w.first + (w.lo + i) % w.tiles) * kTile + half * 64;  // first query of this half
-        const float* st = stats + (it % ST) * 2 * kTile + half * 64;
+        const uint32_t st = smem_u32(stats) + ((it % ST) * 2 * kTile + half * 64) * 4;
         // First column of this half whose query sees the key, 64: none. Queries from it on all do.
         const int from = key >= w.len ? 64 : a.causal ? max(0, key - (w.len - a.Nq) - row) : 0;
         const bool masked = __any_sync(0xffffffffu, from > 0);
@@ -396,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(st + 32 * c + e);
+            const ulonglong2 nl = load_shared16(st + (32 * c + e) * 4);
             const uint64_t x0 = f2_fma(pair_of(&p[c][e]), sc2, nl.x), x1 = f2_fma(pair_of(&p[c][e + 2]), sc2, nl.y);
             const float v[4] = {fast_exp2(f2_lo(x0)), fast_exp2(f2_hi(x0)), fast_exp2(f2_lo(x1)), fast_exp2(f2_hi(x1))};
 #pragma unroll
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(st + kTile + 32 * c + e);
+            const ulonglong2 nd = load_shared16(st + (kTile + 32 * c + e) * 4);
             const uint64_t y0 = f2_mul(f2_add(pair_of(&d[c][e]), nd.x), pair_of(&p[c][e]));
             const uint64_t y1 = f2_mul(f2_add(pair_of(&d[c][e + 2]), nd.y), pair_of(&p[c][e + 2]));
             pk[16 * c + e / 2] = pack_bf16x2(f2_lo(y0), f2_hi(y0));
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t TP = 256, TQ = 384;  // TMEM columns of dP and dQ
   const AttendArgs& a = f.p;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = base;
   uint8_t* sG = sQ + L::TILE;
   uint8_t* ringK = sG + L::TILE;
