@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ float sums[2][kTile];  // narrow: m and l of B's rows
-  __shared__ ItemRing items;
+  __shared__ ItemRing<8> items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int narrow = f.narrow;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b = (g + t) & 1;
           if (!(ok = wait(&p_full[x][b], ((g + t) >> 1) & 1))) break;
           tc_fence_after();
-          issue_ts<D, 0, 4, 32>(lead, ACC + x * 128, x * 128 + b * 64, r0 + sv * L::TILE + e * 8192, t > 0);
+          issue_ts<D, 0, 4, 4, 32>(lead, ACC + x * 128, x * 128 + b * 64, r0 + sv * L::TILE + e * 8192, t > 0);
           commit(&pv_done[x][b]);
           if (e == 1 || t + 1 == nb) commit(&empty[sv]);
           if (j + 1 < n) {

@@ -241,11 +241,11 @@ sla_status launch_backward(const AttendPlan& w, const Maps& m, const AttendRowsA
   SLA_TRY(launch_dependent(sla::attend_rows_kernel<D>, dim3(blocks), dim3(256), 0, st, "attend_rows_kernel", r));
   constexpr int smem_kv = sla::AttendDkvSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dkv_kernel<D>, smem_kv));
-  SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kThreads), smem_kv, st, "attend_dkv_kernel",
+  SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kBwdThreads), smem_kv, st, "attend_dkv_kernel",
                            m.q, m.k, m.v, m.g, kv));
   constexpr int smem_q = sla::AttendDqSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dq_kernel<D>, smem_q));
-  SLA_TRY(launch_dependent(sla::attend_dq_kernel<D>, dim3(w.dq.ctas), dim3(sla::kThreads), smem_q, st, "attend_dq_kernel", m.q,
+  SLA_TRY(launch_dependent(sla::attend_dq_kernel<D>, dim3(w.dq.ctas), dim3(sla::kBwdThreads), smem_q, st, "attend_dq_kernel", m.q,
                            m.k, m.v, m.g, q));
   if (w.dkv.cut || w.dq.cut) {
     const AttendSumArgs s{kv, q, w.dkv.ctas, w.dq.ctas};

@@ -20,6 +20,11 @@
 
 namespace sla {
 
+// A warpgroup for the TMA and MMA warps and four that compute, a quarter of the tile's columns each: the
+// exponentials are bound by latency where a scheduler has two warps to hide it with (dK / dV and dQ
+// kernel at N = 8192: 691 and 643 us with two warpgroups, see below for four).
+constexpr int kBwdWarps = 16, kBwdThreads = 128 + 32 * kBwdWarps;
+
 struct AttendBwdArgs {
   AttendArgs p;
   const float* nlse;    // [B * H, pad] -lse2 (padding rows and rows without keys: -inf)
@@ -100,23 +105,21 @@ __device__ __forceinline__ ulonglong2 load_shared16(uint32_t addr) {
   return v;
 }
 
-// Of columns OFF .. OFF + 31 those before `from` (or, keep_upto, from `upto` on) take `value`.
-template <int OFF>
+// Of 32 columns those before `from` (or, keep_upto, from `upto` on) take `value`.
 __device__ __forceinline__ void keep_from(uint32_t (&x)[32], int from, float value) {
 #pragma unroll
   for (int c = 0; c < 32; ++c)
-    if (OFF + c < from) x[c] = __float_as_uint(value);
+    if (c < from) x[c] = __float_as_uint(value);
 }
-template <int OFF>
 __device__ __forceinline__ void keep_upto(uint32_t (&x)[32], int upto, float value) {
 #pragma unroll
   for (int c = 0; c < 32; ++c)
-    if (OFF + c >= upto) x[c] = __float_as_uint(value);
+    if (c >= upto) x[c] = __float_as_uint(value);
 }
 
 // ---------------------------------------------------------------------------- dK, dV
 
-// One persistent CTA per SM, 384 threads, on units of 128 keys of one key head, a step being a
+// One persistent CTA per SM, 640 threads, on units of 128 keys of one key head, a step being a
 // (query head of the group, query tile) that sees them:
 //   warp 0       TMA: K_j and V_j once, then Q_i, dO_i and the rows' statistics through a ring
 //                of two stages
@@ -124,11 +127,9 @@ __device__ __forceinline__ void keep_upto(uint32_t (&x)[32], int upto, float val
 //                warps form P of tile i the tensor cores run dK of tile i - 1 and dP of tile i;
 //                while they form T, dV of tile i and S of tile i + 1.
 //   warp 2       scheduler: the CTA's units
-//   warps 4..11  thread = key row = TMEM lane; warps 4..7 take the tile's queries 0..63, warps
-//                8..11 queries 64..127
-// TMEM columns: S^T [0,128) and dP^T [128,256), each overwritten by its bf16 result (queries
-// 0..63 at +0, 64..127 at +64, so that each half of the warps overwrites only what it has
-// read); dV [256,256+D), dK [384,384+D).
+//   warps 4..19  thread = key row = TMEM lane; each warpgroup takes 32 of the tile's queries
+// TMEM columns: S^T [0,128) and dP^T [128,256), each overwritten by its bf16 result (32
+// queries' S by 16 columns, so that each warpgroup overwrites only what it has read); dV [256,256+D), dK [384,384+D).
 template <int D>
 struct AttendDkvSmem {
   static constexpr uint32_t TILE = kTile * D * 2;
@@ -179,7 +180,7 @@ struct DkvBarriers {
 // dK += T(i)^T Q_i. Each chain's own order keeps S^T(i + 1) from overwriting P(i), and dP^T(i + 1) T(i).
 // What a product needs besides P or T is looked up before P or T is waited for.
 template <int D, int Y>
-__device__ __forceinline__ void attend_dkv_issue(DkvBarriers<AttendDkvSmem<D>::STAGES>& sh, ItemRing& items,
+__device__ __forceinline__ void attend_dkv_issue(DkvBarriers<AttendDkvSmem<D>::STAGES>& sh, ItemRing<kBwdWarps>& items,
                                                  const AttendBwdArgs& f, uint8_t* kv, uint8_t* ring) {
   using L = AttendDkvSmem<D>;
   constexpr int ST = L::STAGES;
@@ -226,7 +227,7 @@ __device__ __forceinline__ void attend_dkv_issue(DkvBarriers<AttendDkvSmem<D>::S
       if (!(ok = wait(formed, done))) break;
       done ^= 1;
       tc_fence_after();
-      issue_ts<D, 0, 8, 64>(lead, acc, col, smem_u32(tile), i > 0);
+      issue_ts<D, 0, 8, 2, 32>(lead, acc, col, smem_u32(tile), i > 0);
       mma_commit(lead, &free2[cur.s]);
       if (i + 1 == n) mma_commit(lead, &sh.acc_full[Y]);
       cur.next(ST);
@@ -239,7 +240,7 @@ __device__ __forceinline__ void attend_dkv_issue(DkvBarriers<AttendDkvSmem<D>::S
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attend_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g,
                       const __grid_constant__ AttendBwdArgs f) {
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __shared__ DkvBarriers<ST> sh;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ ItemRing items;
+  __shared__ ItemRing<kBwdWarps> items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -264,12 +265,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.kv_free, 2);
     mbar_init(&sh.s_full, 1);
     mbar_init(&sh.dp_full, 1);
-    mbar_init(&sh.p_full, 8);
-    mbar_init(&sh.t_full, 8);
+    mbar_init(&sh.p_full, kBwdWarps);
+    mbar_init(&sh.t_full, kBwdWarps);
     mbar_init(&sh.acc_full[0], 1);
     mbar_init(&sh.acc_full[1], 1);
-    mbar_init(&sh.acc_free[0], 128);
-    mbar_init(&sh.acc_free[1], 128);
+    mbar_init(&sh.acc_free[0], 256);
+    mbar_init(&sh.acc_free[1], 256);
     mbar_init(&sh.drain, 2);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&sh.q_full[s], 1);
@@ -287,13 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_wait();
   const auto steps = [&](int u) { return dkv_unit(a, u, false).tiles * a.G; };
-  AttendWork work = attend_work(a, steps, kThreads);
+  AttendWork work = attend_work(a, steps, kBwdThreads);
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all columns are allocated
   AttendItem item;
 
-  if (warp < 4) regs_down<kIssueRegs>();
   if (warp == kScheduleWarp) {
     if (lane == 0) {
       uint32_t ni = 0;
@@ -363,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       attend_dkv_issue<D, 1>(sh, items, f, sV, ring);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ P and T, then the epilogue
-    regs_up<kComputeRegs>();
-    const int half = warp >= 8;
+    const int quarter = (warp >> 2) - 1;  // of the tile's queries; two of them write dV, two dK
+    const int half = quarter >> 1;
     const int r = (warp & 3) * 32 + lane;  // key row of the tile = TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + half * 64, p_addr = lane_addr + TP + half * 64;
+    const uint32_t s_addr = lane_addr + quarter * 32, p_addr = lane_addr + TP + quarter * 32;
     const float sc = a.scale_log2;
     const uint64_t sc2 = f2_make(sc, sc);
     uint32_t it = 0, nu = 0, ni = 0;
@@ -382,70 +382,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = w.n;
       const int key = w.key0 + r;
       for (int i = 0; i < n; ++i, ++it) {
-        const int row = (w.first + (w.lo + i) % w.tiles) * kTile + half * 64;  // first query of this half
-        const uint32_t st = smem_u32(stats) + ((it % ST) * 2 * kTile + half * 64) * 4;
-        // First column of this half whose query sees the key, 64: none. Queries from it on all do.
-        const int from = key >= w.len ? 64 : a.causal ? max(0, key - (w.len - a.Nq) - row) : 0;
+        const int row = (w.first + (w.lo + i) % w.tiles) * kTile + quarter * 32;  // first query of this quarter
+        const uint32_t st = smem_u32(stats) + ((it % ST) * 2 * kTile + quarter * 32) * 4;
+        // First column of this quarter whose query sees the key, 32: none. Queries from it on all do.
+        const int from = key >= w.len ? 32 : a.causal ? max(0, key - (w.len - a.Nq) - row) : 0;
         const bool masked = __any_sync(0xffffffffu, from > 0);
         if (!(ok = wait(&sh.s_full, it & 1))) break;
         if (!(ok = wait(&sh.q_full[it % ST], (it / ST) & 1))) break;  // the rows' statistics
         tc_fence_after();
-        uint32_t p[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 32 * c, p[c]);
+        uint32_t p[32], pk[16];
+        tmem_ld32(s_addr, p);
         tmem_wait_ld();
-        if (masked) {
-          keep_from<0>(p[0], from, -INFINITY);
-          keep_from<32>(p[1], from, -INFINITY);
+        if (masked) keep_from(p, from, -INFINITY);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 nl = load_shared16(st + e * 4);
+          const uint64_t x0 = f2_fma(pair_of(&p[e]), sc2, nl.x), x1 = f2_fma(pair_of(&p[e + 2]), sc2, nl.y);
+          const float v[4] = {fast_exp2(f2_lo(x0)), fast_exp2(f2_hi(x0)), fast_exp2(f2_lo(x1)), fast_exp2(f2_hi(x1))};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p[e + q] = __float_as_uint(v[q]);
+          pk[e / 2] = pack_bf16x2(v[0], v[1]);
+          pk[e / 2 + 1] = pack_bf16x2(v[2], v[3]);
         }
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 nl = load_shared16(st + (32 * c + e) * 4);
-            const uint64_t x0 = f2_fma(pair_of(&p[c][e]), sc2, nl.x), x1 = f2_fma(pair_of(&p[c][e + 2]), sc2, nl.y);
-            const float v[4] = {fast_exp2(f2_lo(x0)), fast_exp2(f2_hi(x0)), fast_exp2(f2_lo(x1)), fast_exp2(f2_hi(x1))};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) p[c][e + q] = __float_as_uint(v[q]);
-            pk[16 * c + e / 2] = pack_bf16x2(v[0], v[1]);
-            pk[16 * c + e / 2 + 1] = pack_bf16x2(v[2], v[3]);
-          }
-        }
-        tmem_st32(s_addr, pk);
+        tmem_st16(s_addr, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full);
         if (!(ok = wait(&sh.dp_full, it & 1))) break;
         tc_fence_after();
-        uint32_t d[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(p_addr + 32 * c, d[c]);
+        uint32_t d[32];
+        tmem_ld32(p_addr, d);
         tmem_wait_ld();
-        if (masked) {  // dP of a key that is not there may be NaN
-          keep_from<0>(d[0], from, 0.f);
-          keep_from<32>(d[1], from, 0.f);
-        }
+        if (masked) keep_from(d, from, 0.f);  // dP of a key that is not there may be NaN
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 nd = load_shared16(st + (kTile + 32 * c + e) * 4);
-            const uint64_t y0 = f2_mul(f2_add(pair_of(&d[c][e]), nd.x), pair_of(&p[c][e]));
-            const uint64_t y1 = f2_mul(f2_add(pair_of(&d[c][e + 2]), nd.y), pair_of(&p[c][e + 2]));
-            pk[16 * c + e / 2] = pack_bf16x2(f2_lo(y0), f2_hi(y0));
-            pk[16 * c + e / 2 + 1] = pack_bf16x2(f2_lo(y1), f2_hi(y1));
-          }
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 nd = load_shared16(st + (kTile + e) * 4);
+          const uint64_t y0 = f2_mul(f2_add(pair_of(&d[e]), nd.x), pair_of(&p[e]));
+          const uint64_t y1 = f2_mul(f2_add(pair_of(&d[e + 2]), nd.y), pair_of(&p[e + 2]));
+          pk[e / 2] = pack_bf16x2(f2_lo(y0), f2_hi(y0));
+          pk[e / 2 + 1] = pack_bf16x2(f2_lo(y1), f2_hi(y1));
         }
-        tmem_st32(p_addr, pk);
+        tmem_st16(p_addr, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.t_full);
       }
       if (!ok) break;
-      // Warps 4..7 write dV, warps 8..11 dK (times scale); zeros where no query saw the keys.
+      // Two warpgroups write dV, two dK (times scale), half of the channels each; zeros where no query saw
+      // the keys.
       if (n > 0) {
         if (!(ok = wait(&sh.acc_full[half], nu & 1))) break;
         tc_fence_after();
@@ -456,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = f.part + ((static_cast<size_t>(slot) * 2 + (half ? 0 : 1)) * kTile + r) * D;
       __nv_bfloat16* out = o.p + w.b * o.sb + w.hk * o.sh + key * o.sn;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = (quarter & 1) * (D / 2); c0 < ((quarter & 1) + 1) * (D / 2); c0 += 32) {
         uint32_t x[32];
         if (n > 0) {
           tmem_ld32(lane_addr + (half ? TK : TV) + c0, x);
@@ -490,16 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------- dQ
 
-// One persistent CTA per SM, 384 threads, on units of 128 query rows of one head, a step being a
+// One persistent CTA per SM, 640 threads, on units of 128 query rows of one head, a step being a
 // key tile:
 //   warp 0       TMA: Q_i and dO_i once, then K_j and V_j through a ring of two stages
 //   warps 1, 3   tcgen05 issuers: S = Q K^T (two TMEM buffers) and dQ += T K; dP = dO V^T. S and dP of
 //                tile j + 1 run while the warps form T of tile j.
 //   warp 2       scheduler: the CTA's units
-//   warps 4..11  thread = query row = TMEM lane; warps 4..7 take the tile's keys 0..63, warps
-//                8..11 keys 64..127
-// TMEM columns: S ping-pong [0,128) [128,256) (T, bf16, over it: keys 0..63 at +0, 64..127 at
-// +64), dP [256,384), dQ [384,384+D).
+//   warps 4..19  thread = query row = TMEM lane; each warpgroup takes 32 of the tile's keys
+// TMEM columns: S ping-pong [0,128) [128,256) (T, bf16, over it: 16 columns over
+// each 32), dP [256,384), dQ [384,384+D).
 template <int D>
 struct AttendDqSmem {
   static constexpr uint32_t TILE = kTile * D * 2;
@@ -531,7 +516,7 @@ struct DqItem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attend_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g,
                      const __grid_constant__ AttendBwdArgs f) {
@@ -550,20 +535,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t k_full[ST], v_full[ST], k_free[ST], v_free[ST];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  __shared__ ItemRing items;
+  __shared__ ItemRing<kBwdWarps> items;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_free, 2);
     mbar_init(&dp_full, 1);
-    mbar_init(&dp_free, 256);
+    mbar_init(&dp_free, kBwdWarps);
     mbar_init(&acc_full, 1);
-    mbar_init(&acc_free, 256);
+    mbar_init(&acc_free, 32 * kBwdWarps);
     mbar_init(&drain, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&t_full[s], 256);
+      mbar_init(&t_full[s], kBwdWarps);
     }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&k_full[s], 1);
@@ -581,13 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_wait();
   const auto steps = [&](int u) { return dq_unit(a, u, false).tiles; };
-  AttendWork work = attend_work(a, steps, kThreads);
+  AttendWork work = attend_work(a, steps, kBwdThreads);
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all columns are allocated
   AttendItem item;
 
-  if (warp < 4) regs_down<kIssueRegs>();
   if (warp == kScheduleWarp) {
     if (lane == 0) {
       uint32_t ni = 0;
@@ -680,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < n && !(ok = issue_s(j + 1))) break;
         if (!(ok = wait(&t_full[t & 1], (t >> 1) & 1))) break;
         tc_fence_after();
-        issue_ts<D, 0, 8, 64>(lead, TQ, (t & 1) * 128, rk + cur.s * L::TILE, j > 0);
+        issue_ts<D, 0, 8, 2, 32>(lead, TQ, (t & 1) * 128, rk + cur.s * L::TILE, j > 0);
         mma_commit(lead, &k_free[cur.s]);
         if (j + 1 == n) mma_commit(lead, &acc_full);
         cur.next(ST);
@@ -721,8 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(&drain, 0, nullptr, nullptr);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ T, then the epilogue
-    regs_up<kComputeRegs>();
-    const int half = warp >= 8;
+    const int quarter = (warp >> 2) - 1;  // of the tile's keys, then of the channels
     const int r = (warp & 3) * 32 + lane;  // query row of the tile = TMEM lane
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sc = a.scale_log2;
@@ -743,63 +726,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float nl = f.nlse[at], nd = f.ndelta[at];
       const uint64_t nl2 = f2_make(nl, nl), nd2 = f2_make(nd, nd);
       for (int j = 0; j < n; ++j, ++it) {
-        const int key0 = (w.lo + j) * kTile + half * 64;
-        const int upto = end - key0;  // columns of this half that the row sees
-        const bool masked = __any_sync(0xffffffffu, upto < 64);
-        const uint32_t s_addr = lane_addr + (it & 1) * 128 + half * 64;
+        const int key0 = (w.lo + j) * kTile + quarter * 32;
+        const int upto = end - key0;  // columns of this quarter that the row sees
+        const bool masked = __any_sync(0xffffffffu, upto < 32);
+        const uint32_t s_addr = lane_addr + (it & 1) * 128 + quarter * 32;
         if (!(ok = wait(&s_full[it & 1], (it >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t p[2][32], d[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + 32 * c, p[c]);
+        uint32_t p[32], d[32], pk[16];
+        tmem_ld32(s_addr, p);
         tmem_wait_ld();
-        if (masked) {
-          keep_upto<0>(p[0], upto, -INFINITY);
-          keep_upto<32>(p[1], upto, -INFINITY);
-        }
+        if (masked) keep_upto(p, upto, -INFINITY);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x = f2_fma(pair_of(&p[c][e]), sc2, nl2);
-            p[c][e] = __float_as_uint(fast_exp2(f2_lo(x)));
-            p[c][e + 1] = __float_as_uint(fast_exp2(f2_hi(x)));
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t x = f2_fma(pair_of(&p[e]), sc2, nl2);
+          p[e] = __float_as_uint(fast_exp2(f2_lo(x)));
+          p[e + 1] = __float_as_uint(fast_exp2(f2_hi(x)));
         }
         if (!(ok = wait(&dp_full, it & 1))) break;
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(lane_addr + TP + half * 64 + 32 * c, d[c]);
+        tmem_ld32(lane_addr + TP + quarter * 32, d);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(&dp_free);
-        if (masked) {  // dP of a key that is not there may be NaN
-          keep_upto<0>(d[0], upto, 0.f);
-          keep_upto<32>(d[1], upto, 0.f);
-        }
-        uint32_t pk[32];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&dp_free);
+        if (masked) keep_upto(d, upto, 0.f);  // dP of a key that is not there may be NaN
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t y = f2_mul(f2_add(pair_of(&d[c][e]), nd2), pair_of(&p[c][e]));
-            pk[16 * c + e / 2] = pack_bf16x2(f2_lo(y), f2_hi(y));
-          }
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t y = f2_mul(f2_add(pair_of(&d[e]), nd2), pair_of(&p[e]));
+          pk[e / 2] = pack_bf16x2(f2_lo(y), f2_hi(y));
         }
-        tmem_st32(s_addr, pk);
+        tmem_st16(s_addr, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&t_full[it & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_full[it & 1]);
       }
       if (!ok) break;
       if (n > 0) {
         if (!(ok = wait(&acc_full, nu & 1))) break;
         tc_fence_after();
       }
-      // scale times the accumulator: warps 4..7 its first D / 2 channels, warps 8..11 the rest
+      // scale times the accumulator, 32 channels to a warpgroup
       const int slot = w.slot;
-#pragma unroll 1
-      for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+      const int c0 = quarter * 32;
+      if (c0 < D) {
         uint32_t x[32];
         if (n > 0) {
           tmem_ld32(lane_addr + TQ + c0, x);

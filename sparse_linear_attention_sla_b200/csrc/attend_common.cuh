@@ -35,7 +35,6 @@ static_assert(128 * (kIssueRegs + 2 * kComputeRegs) <= kThreads * 168, "more reg
 // wait for a barrier, issue eight MMAs and commit them is over 1000 cycles, about what the tensor
 // cores need for them.
 constexpr int kProducerWarp = 0, kMmaWarp = 1, kScheduleWarp = 2, kMmaWarp2 = 3;
-constexpr int kItemReaders = 11;  // the producer, the MMA warps and the eight computing warps
 
 constexpr int kTile = 128;                 // rows of every tile
 constexpr uint32_t kBox = kTile * 128;     // bytes of one 64-channel box
@@ -174,15 +173,17 @@ struct AttendItem {
 
 // A ring of items in shared memory: one warp fills it while the others are still busy with
 // earlier units, so that finding a unit (divisions, lengths in global memory) costs them nothing.
+template <int COMPUTE_WARPS>
 struct ItemRing {
   static constexpr int SLOTS = 4;
+  static constexpr int READERS = 3 + COMPUTE_WARPS;  // the producer, the MMA warps and the computing warps
   AttendItem item[SLOTS];
   uint64_t full[SLOTS], empty[SLOTS];
 
   __device__ __forceinline__ void init() {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kItemReaders);
+      mbar_init(&empty[s], READERS);
     }
   }
   // By one thread.
@@ -193,7 +194,7 @@ struct ItemRing {
     mbar_arrive(&full[s]);
     return true;
   }
-  // By one thread, as one of kItemReaders.
+  // By one thread, as one of READERS.
   __device__ __forceinline__ bool get_one(uint32_t i, AttendItem& x, uint32_t* err, volatile int* abort_flag) {
     const uint32_t s = i % SLOTS, r = i / SLOTS;
     if (!mbar_wait(&full[s], r & 1, err, abort_flag)) return false;
@@ -201,7 +202,7 @@ struct ItemRing {
     mbar_arrive(&empty[s]);
     return true;
   }
-  // By a whole warp (one of kItemReaders); false: the wait ran out.
+  // By a whole warp (one of READERS); false: the wait ran out.
   __device__ __forceinline__ bool get(uint32_t i, AttendItem& x, uint32_t* err, volatile int* abort_flag) {
     const uint32_t s = i % SLOTS, r = i / SLOTS;
     if (!warp_wait(&full[s], r & 1, err, abort_flag)) return false;
@@ -301,19 +302,19 @@ __device__ __forceinline__ void issue_ss(uint32_t lead, uint32_t d_tmem, uint32_
 }
 
 // D[128 x D] (+)= P B over the rows [16 K0, 16 K1) of the tile at b_smem. P's 16-row steps are 8 TMEM
-// columns each; the columns of rows 64.. start GAP columns behind those of rows 0..
-template <int D, int K0, int K1, int GAP>
+// columns each; after every GROUP steps P's columns go on GAP columns behind the group's first.
+template <int D, int K0, int K1, int GROUP, int GAP>
 __device__ __forceinline__ void issue_ts(uint32_t lead, uint32_t d_tmem, uint32_t p_tmem, uint32_t b_smem,
                                          bool accumulate) {
   constexpr uint32_t id = idesc_bf16_f32(128, D, 0, 1);
   const uint32_t bd = uniform(desc_lo(b_smem, kBox));
   if (accumulate)
-    mma_ts(lead, d_tmem, p_tmem + (K0 >> 2) * GAP + (K0 & 3) * 8, desc_of(bd + (K0 * 2048 >> 4)), id, true);
+    mma_ts(lead, d_tmem, p_tmem + K0 / GROUP * GAP + K0 % GROUP * 8, desc_of(bd + (K0 * 2048 >> 4)), id, true);
   else
-    mma_ts(lead, d_tmem, p_tmem + (K0 >> 2) * GAP + (K0 & 3) * 8, desc_of(bd + (K0 * 2048 >> 4)), id, false);
+    mma_ts(lead, d_tmem, p_tmem + K0 / GROUP * GAP + K0 % GROUP * 8, desc_of(bd + (K0 * 2048 >> 4)), id, false);
 #pragma unroll
   for (int kk = K0 + 1; kk < K1; ++kk)
-    mma_ts(lead, d_tmem, p_tmem + (kk >> 2) * GAP + (kk & 3) * 8, desc_of(bd + (kk * 2048 >> 4)), id, true);
+    mma_ts(lead, d_tmem, p_tmem + kk / GROUP * GAP + kk % GROUP * 8, desc_of(bd + (kk * 2048 >> 4)), id, true);
 }
 
 // A place in a ring of n stages: its index, and the parity of its current round.
