@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();  // lengths and inputs may come from earlier kernels
+  grid_dep_launch();
   const auto steps = [&](int u) { return attend_unit(f, u, false).steps(narrow); };
   AttendWork work = attend_work(a, steps, kThreads);
   __syncthreads();
@@ -519,6 +520,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   constexpr int T = D / 8;
   const AttendArgs& a = f.p;
   grid_dep_wait();
+  grid_dep_launch();
   const int C = gridDim.x, c0 = blockIdx.x;
   const int4 meta = a.meta[c0];
   if (meta.x < 0) return;
@@ -527,21 +529,37 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const AttendUnit w = attend_unit(f, meta.x, false);
   int h, i;
   if (!attend_row(f, w, row / kTile, row % kTile, h, i)) return;
-  // Slots: 2 c0 + 1, then 2 k of every later CTA k up to meta.y.
+  // Slots: 2 c0 + 1, then 2 k of every later CTA k up to meta.y; four parts' loads in flight.
   float m = -INFINITY, sum = 0.f, acc[8] = {};
-  for (int k = c0; k <= meta.y; ++k) {
-    if (part_is_empty(meta.z, C, k)) continue;
-    const size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k) * rows + row;
-    const float lse2 = f.part_lse2[at];
-    const float4* p = reinterpret_cast<const float4*>(f.part + at * D + c);
-    const float4 u = p[0], v = p[1];
-    const float top = fmaxf(m, lse2);
-    if (top == -INFINITY) continue;  // no part has seen a key yet
-    const float g = exp2f(m - top), e = exp2f(lse2 - top);
-    const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    sum = sum * g + e;
+  for (int k0 = c0; k0 <= meta.y; k0 += 4) {
+    float lse2[4];
+    float4 x[4], y[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] = acc[q] * g + e * x[q];
+    for (int p = 0; p < 4; ++p) {
+      const int k = k0 + p;
+      lse2[p] = -INFINITY;
+      x[p] = y[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k > meta.y || part_is_empty(meta.z, C, k)) continue;
+      const size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k) * rows + row;
+      const float4* v = reinterpret_cast<const float4*>(f.part + at * D + c);
+      lse2[p] = f.part_lse2[at];
+      x[p] = v[0];
+      y[p] = v[1];
+    }
+    const float top = fmaxf(fmaxf(fmaxf(lse2[0], lse2[1]), fmaxf(lse2[2], lse2[3])), m);
+    if (top == -INFINITY) continue;  // no part has seen a key yet
+    const float g = exp2f(m - top);
+    sum *= g;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] *= g;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float e = exp2f(lse2[p] - top);
+      const float v[8] = {x[p].x, x[p].y, x[p].z, x[p].w, y[p].x, y[p].y, y[p].z, y[p].w};
+      sum += e;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] = fmaf(e, v[q], acc[q]);
+    }
     m = top;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(256) attend_rows_kernel(AttendRowsArgs a) {
   const int row0 = blockIdx.x % per_head * (256 / T * U) + threadIdx.x / T;
   const int c = (threadIdx.x % T) * 8;
   grid_dep_wait();
+  grid_dep_launch();
   const int b = bh / a.H, h = bh % a.H;
   const __nv_bfloat16* const out = a.out + b * a.ob + h * a.oh + c;
   const __nv_bfloat16* const dO = a.dO + b * a.gb + h * a.gh + c;
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();
+  grid_dep_launch();
   const auto steps = [&](int u) { return dkv_unit(a, u, false).tiles * a.G; };
   AttendWork work = attend_work(a, steps, kBwdThreads);
   __syncthreads();
@@ -565,6 +567,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();
+  grid_dep_launch();
   const auto steps = [&](int u) { return dq_unit(a, u, false).tiles; };
   AttendWork work = attend_work(a, steps, kBwdThreads);
   __syncthreads();
@@ -813,6 +816,7 @@ template <int D>
 __global__ void __launch_bounds__(256) attend_sum_kernel(const __grid_constant__ AttendSumArgs s) {
   constexpr int T = D / 8;
   grid_dep_wait();
+  grid_dep_launch();
   const bool is_q = blockIdx.z == 2;
   const AttendBwdArgs& f = is_q ? s.q : s.kv;
   const AttendArgs& a = f.p;
@@ -833,14 +837,24 @@ __global__ void __launch_bounds__(256) attend_sum_kernel(const __grid_constant__
     out = o.p + w.b * o.sb + w.hk * o.sh + (w.key0 + r) * o.sn + c;
   }
   float x[8] = {};
-#pragma unroll 4
-  for (int k = c0; k <= meta.y; ++k) {
-    if (part_is_empty(meta.z, C, k)) continue;
-    size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k);
-    if (!is_q) at = at * 2 + blockIdx.z;
-    const float4* p = reinterpret_cast<const float4*>(f.part + (at * kTile + r) * D + c);
-    const float4 u = p[0], v = p[1];
-    x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w, x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
+  for (int k0 = c0; k0 <= meta.y; k0 += 4) {
+    float4 u[4], v[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int k = k0 + p;
+      u[p] = v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k > meta.y || part_is_empty(meta.z, C, k)) continue;
+      size_t at = static_cast<size_t>(k == c0 ? 2 * k + 1 : 2 * k);
+      if (!is_q) at = at * 2 + blockIdx.z;
+      const float4* w = reinterpret_cast<const float4*>(f.part + (at * kTile + r) * D + c);
+      u[p] = w[0];
+      v[p] = w[1];
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      x[0] += u[p].x, x[1] += u[p].y, x[2] += u[p].z, x[3] += u[p].w;
+      x[4] += v[p].x, x[5] += v[p].y, x[6] += v[p].z, x[7] += v[p].w;
+    }
   }
   *reinterpret_cast<uint4*>(out) =
       make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));

@@ -116,9 +116,27 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
   const int h1 = min(h0 + a.heads_per_block, a.heads[0] + a.heads[1]);
   const bool in = n < a.N;
 
+  const long long xq = b * a.t[0].xb + n * a.t[0].xn + c0, xk = b * a.t[1].xb + n * a.t[1].xn + c0;
+  const long long yq = b * a.t[0].yb + n * a.t[0].yn + c0, yk = b * a.t[1].yb + n * a.t[1].yn + c0;
+  RotaryChunk<Tin> x[U];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (in && h + u < h1) {
+        const int hk = h + u - a.heads[0];
+        x[u].load(hk < 0 ? static_cast<const Tin*>(a.t[0].x) + xq + (h + u) * a.t[0].xh
+                         : static_cast<const Tin*>(a.t[1].x) + xk + hk * a.t[1].xh);
+      }
+    }
+  };
+  load(h0);  // the first heads are under way while the angles are formed
+
   // The block's frequencies, one for each pair of channels, then this thread's angles. Pairs of
   // neighbours lie in one thread; halves share theirs through the table of all tokens' pairs.
-  __shared__ double freq[D / 2];
+  // A frequency is held as its fraction of a turn in 64 bits (whole turns per step drop out, positions
+  // being whole), so an angle is one integer product, reduced by its overflow: off by at most 2^-33 of a
+  // turn plus |p| times the fp64 rounding of the frequency.
+  __shared__ uint2 freq[D / 2];
   __shared__ float2 table[HALVES ? TOKENS * (D / 2) : 1];
   const int turned_channels = a.first[a.n_axes];
   auto axis_of = [&](int c) {
@@ -128,24 +146,33 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
   };
   if (threadIdx.x < D / 2 && 2 * threadIdx.x < turned_channels) {
     const int ax = axis_of(2 * threadIdx.x), d = a.first[ax + 1] - a.first[ax];
-    freq[threadIdx.x] = exp2(-static_cast<double>(2 * threadIdx.x - a.first[ax]) / d * a.log2_base);
+    const double f = exp2(-static_cast<double>(2 * threadIdx.x - a.first[ax]) / d * a.log2_base) * 0.15915494309189535;
+    const unsigned long long u = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
+    freq[threadIdx.x] = make_uint2(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32));
+  }
+  const bool turns = in && (a.pos || n < a.n_turned);
+  int at[kMaxAxes] = {};  // the token's position on each axis
+  if (turns) {
+    int q = n;
+#pragma unroll
+    for (int x = kMaxAxes - 1; x >= 0; --x) {
+      if (x >= a.n_axes) continue;
+      if (a.pos) {
+        at[x] = a.pos[b * a.pos_b + static_cast<long long>(n) * a.n_axes + x];
+      } else {
+        at[x] = q % a.grid[x] + a.start[x];
+        q /= a.grid[x];
+      }
+    }
   }
   __syncthreads();
-  const bool turns = in && (a.pos || n < a.n_turned);
-  // cos and sin of pair p (counted over all axes) at token n: the angle in fp64, brought into
-  // [-pi, pi] with 2 pi as a sum of two doubles.
+  // cos and sin of pair p (counted over all axes) on axis ax.
   auto angle = [&](int p, int ax, float& co, float& s) {
-    int at;
-    if (a.pos) {
-      at = a.pos[b * a.pos_b + static_cast<long long>(n) * a.n_axes + ax];
-    } else {
-      int q = n;
-      for (int x = a.n_axes - 1; x > ax; --x) q /= a.grid[x];
-      at = q % a.grid[ax] + a.start[ax];
-    }
-    const double phi = at * freq[p];
-    const double full = rint(phi * 0.15915494309189535);
-    sincosf(static_cast<float>(fma(-full, 2.4492935982947064e-16, fma(-full, 6.283185307179586, phi))), &s, &co);
+    const uint32_t v = ax == 0 ? at[0] : ax == 1 ? at[1] : ax == 2 ? at[2] : at[3];
+    const uint2 f = freq[p];
+    // Bits 32..63 of v f modulo 2^64: a negative v, taken as v + 2^32, adds f.x there.
+    const uint32_t turn = v * f.y + __umulhi(v, f.x) - (static_cast<int>(v) < 0 ? f.x : 0u);
+    sincospif(static_cast<float>(static_cast<int>(turn)) * 0x1p-31f, &s, &co);
     s *= a.sign;
   };
 
@@ -194,18 +221,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
     }
   }
 
-  const long long xq = b * a.t[0].xb + n * a.t[0].xn + c0, xk = b * a.t[1].xb + n * a.t[1].xn + c0;
-  const long long yq = b * a.t[0].yb + n * a.t[0].yn + c0, yk = b * a.t[1].yb + n * a.t[1].yn + c0;
   for (int h = h0; h < h1; h += U) {
-    RotaryChunk<Tin> x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (in && h + u < h1) {
-        const int hk = h + u - a.heads[0];
-        x[u].load(hk < 0 ? static_cast<const Tin*>(a.t[0].x) + xq + (h + u) * a.t[0].xh
-                         : static_cast<const Tin*>(a.t[1].x) + xk + hk * a.t[1].xh);
-      }
-    }
+    if (h > h0) load(h);
     if (HALVES) {
       __syncwarp();  // the previous heads' partners have been read
 #pragma unroll
