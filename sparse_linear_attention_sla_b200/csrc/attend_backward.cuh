@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
-  grid_dep_wait();
+  // Runs beside attend_dkv_kernel where SMs are free: that kernel's CTAs let this one in after their own wait for
+  // attend_rows_kernel, whose results are all that this one needs of earlier kernels. The wait comes last.
   grid_dep_launch();
   const auto steps = [&](int u) { return dq_unit(a, u, false).tiles; };
   AttendWork work = attend_work(a, steps, kBwdThreads);
@@ -796,6 +797,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
   }
+  grid_dep_wait();  // this kernel is not done before attend_dkv_kernel is
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {

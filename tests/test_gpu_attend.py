@@ -120,6 +120,26 @@ def test_moving_reference(cuda_device, D):
     _check(q, first, v, dO)
 
 
+def test_scores_near_the_end_of_the_range(cuda_device):
+    """Scores of 1e38, whose rounding alone passes what an exponential can hold: whatever comes out, it comes, and the
+    other rows are as they are without it."""
+    q, k, v, dO = _make(14, 1, 2, 2, 140, 300, 128, cuda_device)
+    want, wlse = binding.attend(q, k, v)
+    big = q.clone()
+    big[:, :, 7] = 3e37
+    p = binding.attend_problem(big, k)
+    ws = binding.new_workspace_attend(p, cuda_device)
+    out, lse = binding.attend(big, k, v, ws=ws)
+    binding.check(ws)
+    keep = torch.arange(140, device=cuda_device) != 7
+    assert torch.equal(out[:, :, keep], want[:, :, keep]) and torch.equal(lse[:, :, keep], wlse[:, :, keep])
+    for Nq in (1, 40):  # one tile, most of whose rows are no query
+        ws = binding.new_workspace_attend(binding.attend_problem(big[:, :, 7:7 + Nq], k), cuda_device)
+        out, _ = binding.attend(big[:, :, 7:7 + Nq], k, v, ws=ws)
+        binding.check(ws)
+        assert torch.equal(out[:, :, 1:], binding.attend(q[:, :, 7:7 + Nq], k, v)[0][:, :, 1:])
+
+
 def test_scale(cuda_device):
     q, k, v, dO = _make(9, 1, 2, 2, 150, 333, 128, cuda_device)
     for scale in (1e-4, 0.5):
