@@ -540,21 +540,24 @@ def rotary_spec(axes, grid=None, positions=None, start=None, base=10000.0, pairi
 
 
 def _check_heads(name, t, B, H, N, D, dtype, device):
-    """A [B, H, N, D] tensor whose channels are contiguous (the library checks the other strides)."""
+    """A [B, H, N, D] tensor whose channels are contiguous (the library checks the other strides), as
+    the library takes it."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.shape != (B, H, N, D) or (D > 1 and t.stride(3) != 1):
+    if t.dtype is not dtype or t.shape != (B, H, N, D) or t.stride(3) != 1:
         raise ValueError(f"{name} must be {dtype} of shape {(B, H, N, D)} with contiguous channels, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    b, h, n, _ = t.stride()
+    return Tensor(t.data_ptr(), b, h, n)
 
 
-def _tensor(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    s = t.stride()
-    return Tensor(t.data_ptr(), s[0], s[1], s[2])
+def _new_heads(like, B, H, N, D, dtype):
+    """A contiguous [B, H, N, D] tensor on `like`'s device, and as the library takes it."""
+    t = like.new_empty((B, H, N, D), dtype=dtype)
+    n = N * D
+    return t, Tensor(t.data_ptr(), H * n, n, D)
 
 
 def _address(t: Optional[torch.Tensor]):
@@ -611,25 +614,21 @@ def _rotary_call(q, k, spec, out, dtype, names, backward):
     pos = spec.positions_tensor
     if pos is not None and (pos.device != dev or pos.shape[-2] != N or (pos.dim() == 3 and pos.shape[0] != B)):
         raise ValueError(f"positions {tuple(pos.shape)} on {pos.device} do not fit {B} sequences of {N} tokens on {dev}")
-    heads, outs = [], []
-    given = out if out is not None else (None, None)
-    for name, x, y in zip(names, (q, k), given):
+    outs, args, heads = [None, None], [None] * 4, [0, 0]
+    for w, x in enumerate((q, k)):
         if x is None:
-            heads.append(0)
-            outs.append(None)
             continue
-        H = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 4 else 0
-        _check_heads(name, x, B, H, N, D, in_dtype, dev)
+        H = heads[w] = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 4 else 0
+        args[2 * w] = _check_heads(names[w], x, B, H, N, D, in_dtype, dev)
+        y = out[w] if out is not None else None
         if y is None:
-            y = torch.empty(B, H, N, D, dtype=dtype, device=dev)
+            outs[w], args[2 * w + 1] = _new_heads(x, B, H, N, D, dtype)
         else:
-            _check_heads(f"out of {name}", y, B, H, N, D, dtype, dev)
-            _check_in_place(f"out of {name}", x, y)
-        heads.append(H)
-        outs.append(y)
+            args[2 * w + 1] = _check_heads(f"out of {names[w]}", y, B, H, N, D, dtype, dev)
+            _check_in_place(f"out of {names[w]}", x, y)
+            outs[w] = y
     lib, call = load_library(), _Call(dev)
-    args = (_tensor(q), _tensor(outs[0]), _tensor(k), _tensor(outs[1]))
-    in_code, out_code = int(in_dtype == torch.float32), int(dtype == torch.float32)  # SLA_BF16, SLA_F32
+    in_code, out_code = int(in_dtype is torch.float32), int(dtype is torch.float32)  # SLA_BF16, SLA_F32
     if backward:
         call(lib.sla_rotary_backward, spec, B, heads[0], heads[1], N, D, in_code, out_code, *args)
     else:
@@ -679,15 +678,14 @@ def _attend_space(p, device, backward):
 
 def _attend_inputs(q, k, v, kv_lens, causal, scale):
     p = attend_problem(q, k, causal, scale)
-    dev = q.device
-    _check_heads("q", q, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    _check_heads("k", k, p.B, p.Hk, p.Nk, p.D, torch.bfloat16, dev)
-    _check_heads("v", v, p.B, p.Hk, p.Nk, p.D, torch.bfloat16, dev)
+    dev, bf16 = q.device, torch.bfloat16
+    args = (_check_heads("q", q, p.B, p.H, p.Nq, p.D, bf16, dev), _check_heads("k", k, p.B, p.Hk, p.Nk, p.D, bf16, dev),
+            _check_heads("v", v, p.B, p.Hk, p.Nk, p.D, bf16, dev))
     if kv_lens is not None and (not isinstance(kv_lens, torch.Tensor) or kv_lens.dtype != torch.int32
                                 or tuple(kv_lens.shape) != (p.B,) or not kv_lens.is_contiguous()
                                 or kv_lens.device != dev):
         raise ValueError(f"kv_lens must be contiguous int32 [{p.B}] on {dev}")
-    return p, dev
+    return p, dev, args
 
 
 def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
@@ -697,34 +695,34 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
     divides H. kv_lens: int32 [B] keys of each sequence (None: Nk). causal: query i sees the keys
     j <= i + len - Nq. scale: 1 / sqrt(D) if None. A query without keys gives 0 and lse = -inf.
     ws: new_workspace_attend's, kept where a device-side error is to be asked for with check(ws)."""
-    p, dev = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    p, dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
     if out is None:
-        out = torch.empty(p.B, p.H, p.Nq, p.D, dtype=torch.bfloat16, device=dev)
+        out, o = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
     else:
-        _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    lse = torch.empty(p.B, p.H, p.Nq, dtype=torch.float32, device=dev)
+        o = _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    lse = q.new_empty((p.B, p.H, p.Nq), dtype=torch.float32)
     if ws is None:
         ws = _attend_space(p, dev, False)
-    _Call(dev)(load_library().sla_attend, p, _tensor(q), _tensor(k), _tensor(v), _address(kv_lens), _tensor(out),
-               lse.data_ptr(), ws.data_ptr(), ws.numel())
+    _Call(dev)(load_library().sla_attend, p, *args, _address(kv_lens), o, lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
 
 
 def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=None, ws=None):
     """sla_attend_backward: (dq [B,H,Nq,D], dk, dv [B,Hk,Nk,D]) bf16 of sum(dO * out), from attend's
     out and lse of the same arguments. Equal calls give equal bits."""
-    p, dev = _attend_inputs(q, k, v, kv_lens, causal, scale)
-    _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    _check_heads("dO", dO, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != (p.B, p.H, p.Nq) \
+    p, dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    o = _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    g = _check_heads("dO", dO, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.shape != (p.B, p.H, p.Nq) \
             or not lse.is_contiguous() or lse.device != dev:
         raise ValueError(f"lse must be contiguous fp32 [{p.B}, {p.H}, {p.Nq}] on {dev}")
-    dq = torch.empty(p.B, p.H, p.Nq, p.D, dtype=torch.bfloat16, device=dev)
-    dk, dv = (torch.empty(p.B, p.Hk, p.Nk, p.D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    dq, a = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
+    dk, b = _new_heads(k, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
+    dv, c = _new_heads(v, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
     if ws is None:
         ws = _attend_space(p, dev, True)
-    _Call(dev)(load_library().sla_attend_backward, p, _tensor(q), _tensor(k), _tensor(v), _tensor(out), lse.data_ptr(),
-               _tensor(dO), _address(kv_lens), _tensor(dq), _tensor(dk), _tensor(dv), ws.data_ptr(), ws.numel())
+    _Call(dev)(load_library().sla_attend_backward, p, *args, o, lse.data_ptr(), g, _address(kv_lens), a, b, c,
+               ws.data_ptr(), ws.numel())
     return dq, dk, dv
 
 
