@@ -290,8 +290,9 @@ def route_variant(q, k, block_q, block_kv, kh, kl, feature_map=0, block_score=0,
 
 
 def forward_variant(q, k, v, alpha, block_q, block_kv, kh, kl, feature_map=0, block_score=0, mask=None, out=None,
-                    ws=None, linear_scale=0.0, drop_threshold=0.0):
-    """sla_forward_variant: O [B,H,N,D] bf16."""
+                    ws=None, linear_scale=0.0, drop_threshold=0.0, rotary_by=None):
+    """sla_forward_variant: O [B,H,N,D] bf16. rotary_by: as for forward."""
+    q, k = _rotated(q, k, rotary_by)
     p, out, ws = _forward_args(q, k, v, alpha, block_q, block_kv, kh, kl, mask, out, ws)
     var = Variant(feature_map, block_score, float(linear_scale), float(drop_threshold))
     lib = load_library()
@@ -304,8 +305,11 @@ def forward_variant(q, k, v, alpha, block_q, block_kv, kh, kl, feature_map=0, bl
     return out
 
 
-def backward(q, k, v, alpha, dO, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, ws=None):
-    """sla_backward: (dQ, dK, dV [B,H,N,D] fp32, dalpha [H,D] fp32) of sum(dO * O)."""
+def backward(q, k, v, alpha, dO, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, ws=None, rotary_by=None):
+    """sla_backward: (dQ, dK, dV [B,H,N,D] fp32, dalpha [H,D] fp32) of sum(dO * O).
+
+    rotary_by: as for forward; dQ and dK are then the gradients of the q and k given here."""
+    q, k = _rotated(q, k, rotary_by)
     B, H, N, D = q.shape
     dev = q.device
     for name, t in (("q", q), ("k", k), ("v", v), ("dO", dO)):
@@ -331,6 +335,8 @@ def backward(q, k, v, alpha, dO, block_q=128, block_kv=64, kh=0.05, kl=0.10, mas
                               _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dalpha), _ptr(ws), ctypes.c_size_t(ws.numel()),
                               _stream_handle(dev))
     _raise(st)
+    if rotary_by is not None:
+        rotary_backward(dQ, dK, rotary_by, out=(dQ, dK))
     return dQ, dK, dV, dalpha, ws
 
 
@@ -362,8 +368,11 @@ def new_workspace_pisa(p: Problem, device) -> torch.Tensor:
     return ws
 
 
-def forward_pisa(q, k, v, block_q=128, block_kv=64, kh=0.05, kl=0.10, labels=None, out=None, ws=None):
-    """sla_forward_pisa: O [B,H,N,D] bf16. labels [B,H,Nq,Nk] int8 (2 = critical) or None (the router)."""
+def forward_pisa(q, k, v, block_q=128, block_kv=64, kh=0.05, kl=0.10, labels=None, out=None, ws=None,
+                 rotary_by=None):
+    """sla_forward_pisa: O [B,H,N,D] bf16. labels [B,H,Nq,Nk] int8 (2 = critical) or None (the router).
+    rotary_by: as for forward."""
+    q, k = _rotated(q, k, rotary_by)
     B, H, N, D = q.shape
     dev = q.device
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -433,8 +442,18 @@ def _forward_args(q, k, v, alpha, block_q, block_kv, kh, kl, mask, out, ws, fp8=
     return p, out, ws
 
 
-def forward(q, k, v, alpha, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, out=None, ws=None):
-    """Fused SLA forward: O = alpha * O_s + (1 - alpha) * O_l, bf16 [B,H,N,D]."""
+def _rotated(q, k, spec):
+    """q and k as the attention takes them: themselves, or turned by the rotary_spec."""
+    return (q, k) if spec is None else rotary(q, k, spec)
+
+
+def forward(q, k, v, alpha, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, out=None, ws=None,
+            rotary_by=None):
+    """Fused SLA forward: O = alpha * O_s + (1 - alpha) * O_l, bf16 [B,H,N,D].
+
+    rotary_by: a rotary_spec by whose positions q and k are turned first. They may then have any
+    strides with contiguous channels (a projection's [B,N,H,D] output as its transpose(1, 2))."""
+    q, k = _rotated(q, k, rotary_by)
     p, out, ws = _forward_args(q, k, v, alpha, block_q, block_kv, kh, kl, mask, out, ws)
     lib = load_library()
     with torch.cuda.device(q.device):
@@ -458,8 +477,10 @@ def forward_timed(q, k, v, alpha, block_q=128, block_kv=64, kh=0.05, kl=0.10, ma
     return out, [float(x) for x in ms]
 
 
-def forward_fp8(q, k, v, alpha, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, out=None, ws=None):
+def forward_fp8(q, k, v, alpha, block_q=128, block_kv=64, kh=0.05, kl=0.10, mask=None, out=None, ws=None,
+                rotary_by=None):
     """forward() with the low-bit (e4m3) sparse branch (include/sla.h states the reading); D = 128."""
+    q, k = _rotated(q, k, rotary_by)
     p, out, ws = _forward_args(q, k, v, alpha, block_q, block_kv, kh, kl, mask, out, ws, fp8=True)
     lib = load_library()
     with torch.cuda.device(q.device):

@@ -241,3 +241,53 @@ def test_pisa_host_checks(lib):
     bad = binding.problem(1, 2, 1000, 96, 128, 64, 0.25, 0.25)
     assert lib.sla_workspace_size_pisa(ctypes.byref(bad)) == 0
     assert lib.sla_forward_pisa(ctypes.byref(bad), fake, fake, fake, null, out, ws, size, null) == 2
+
+
+def test_rotary_host_checks(lib):
+    spec = lambda **kw: binding.rotary_spec((32, 32), grid=(4, 5), **kw)  # noqa: E731
+    t = binding.Tensor(1 << 20, 64 * 20 * 2, 64 * 20, 64)  # aligned, never dereferenced on the host
+    call = lambda s, B=1, Hq=2, Hk=2, N=20, D=64, ty=0, q=t, qo=t, k=t, ko=t: lib.sla_rotary(  # noqa: E731
+        s, B, Hq, Hk, N, D, ty, q, qo, k, ko, None)
+    assert call(None) == 1
+    assert call(spec(), B=0) == 1 and call(spec(), N=0) == 1 and call(spec(), Hq=0, Hk=0) == 1 and call(spec(), Hq=-1) == 1
+    assert call(spec(), D=96) == 2 and call(spec(), ty=7) == 2 and call(spec(), B=70000) == 2
+    assert call(spec(), q=None) == 1 and call(spec(), ko=None) == 1
+    assert call(spec(), q=binding.Tensor((1 << 20) + 8, 2560, 1280, 64)) == 1   # pointer
+    assert call(spec(), q=binding.Tensor(1 << 20, 2560, 1284, 64)) == 1         # stride
+    assert call(spec(base=-1.0)) == 1 and call(spec(base=float("inf"))) == 1 and call(spec(pairing=3)) == 1
+    assert call(spec(start=(2 ** 31 - 2, 0))) == 1                               # positions past 32 bits
+    odd, wide, none = spec(), spec(), spec()
+    odd.channels[1], wide.channels[1], none.n_axes = 31, 34, 0
+    assert call(odd) == 1 and call(wide) == 1 and call(none) == 1
+    back = lambda i, o: lib.sla_rotary_backward(spec(), 1, 2, 2, 20, 64, i, o, None, t, t, t, None)  # noqa: E731
+    assert back(0, 1) == 2      # bf16 gradients as fp32
+    assert back(1, 0) == 1      # allowed types: the NULL tensor is refused
+
+
+def test_attend_host_checks(lib):
+    P = lambda B=1, H=4, Hk=2, Nq=20, Nk=30, D=64, causal=0, scale=0.125: binding.AttendProblem(  # noqa: E731
+        B, H, Hk, Nq, Nk, D, causal, scale)
+    for bad, status in ((P(B=0), 1), (P(Nq=0), 1), (P(Nk=0), 1), (P(Hk=0), 1), (P(H=3), 1), (P(D=96), 2), (P(causal=2), 1),
+                        (P(scale=0.0), 1), (P(scale=float("nan")), 1), (P(scale=float("inf")), 1), (P(Nk=2 ** 24 + 1), 2),
+                        (P(B=2 ** 20, H=2 ** 10, Hk=1, Nq=1), 2)):
+        assert lib.sla_workspace_size_attend(bad) == 0 and lib.sla_workspace_size_attend_backward(bad) == 0
+        assert lib.sla_attend(bad, None, None, None, None, None, None, None, 0, None) == status
+    p = P()
+    n = lib.sla_workspace_size_attend(p)
+    assert n >= 256 and n % 256 == 0
+    q = binding.Tensor(1 << 20, 4 * 20 * 64, 20 * 64, 64)
+    k = binding.Tensor(2 << 20, 2 * 30 * 64, 30 * 64, 64)
+    ws = 16 << 20
+    call = lambda q=q, k=k, v=k, o=q, lens=None, lse=1 << 21, w=ws, b=n, p=p: lib.sla_attend(  # noqa: E731
+        p, q, k, v, lens, o, lse, w, b, None)
+    assert call(q=None) == 1 and call(v=None) == 1 and call(o=None) == 1 and call(lse=None) == 1 and call(lse=2) == 1
+    assert call(lens=2) == 1
+    assert call(k=binding.Tensor(2 << 20, 3840, 1920, 60)) == 1      # rows of 120 bytes
+    assert call(k=binding.Tensor(2 << 20, 3840, 0, 64)) == 1         # a broadcast head
+    assert call(k=binding.Tensor(2 << 20, 3840, -1920, 64)) == 1
+    assert call(k=binding.Tensor(2 << 20, 3840, 1920, 1 << 38)) == 2
+    assert call(w=None) == 3 and call(w=ws + 16) == 3 and call(b=255) == 3
+    # one workspace size for calls with and without lengths, whatever is cut
+    for shape in (P(Nq=1, Nk=32760, H=40, Hk=8, D=128), P(Nq=2040, Nk=2040, H=16, Hk=4), P(Nq=32760, Nk=512, H=12, Hk=12, D=128)):
+        assert 256 <= lib.sla_workspace_size_attend(shape) < 1 << 27
+        assert lib.sla_workspace_size_attend_backward(shape) < 1 << 27
