@@ -239,14 +239,19 @@ sla_status launch_backward(const AttendPlan& w, const Maps& m, const AttendRowsA
   constexpr int per = 256 / (D / 8);
   const unsigned blocks = static_cast<unsigned>(w.p.B) * w.p.H * (w.pad / (per * sla::kRowsUnroll));
   SLA_TRY(launch_dependent(sla::attend_rows_kernel<D>, dim3(blocks), dim3(256), 0, st, "attend_rows_kernel", r));
-  constexpr int smem_kv = sla::AttendDkvSmem<D>::total();
+  constexpr int smem_kv = sla::AttendDkvSmem<D>::total(), smem_q = sla::AttendDqSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dkv_kernel<D>, smem_kv));
-  SLA_TRY(launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kBwdThreads), smem_kv, st, "attend_dkv_kernel",
-                           m.q, m.k, m.v, m.g, kv));
-  constexpr int smem_q = sla::AttendDqSmem<D>::total();
   SLA_TRY(allow_smem(sla::attend_dq_kernel<D>, smem_q));
-  SLA_TRY(launch_dependent(sla::attend_dq_kernel<D>, dim3(w.dq.ctas), dim3(sla::kBwdThreads), smem_q, st, "attend_dq_kernel", m.q,
-                           m.k, m.v, m.g, q));
+  auto run_dkv = [&] {
+    return launch_dependent(sla::attend_dkv_kernel<D>, dim3(w.dkv.ctas), dim3(sla::kBwdThreads), smem_kv, st,
+                            "attend_dkv_kernel", m.q, m.k, m.v, m.g, kv);
+  };
+  auto run_dq = [&] {
+    return launch_dependent(sla::attend_dq_kernel<D>, dim3(w.dq.ctas), dim3(sla::kBwdThreads), smem_q, st,
+                            "attend_dq_kernel", m.q, m.k, m.v, m.g, q);
+  };
+  SLA_TRY(q.dq_first ? run_dq() : run_dkv());
+  SLA_TRY(q.dq_first ? run_dkv() : run_dq());
   if (w.dkv.cut || w.dq.cut) {
     const AttendSumArgs s{kv, q, w.dkv.ctas, w.dq.ctas};
     const int ctas = w.dkv.ctas > w.dq.ctas ? w.dkv.ctas : w.dq.ctas;
@@ -336,6 +341,8 @@ sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q,
   f.nlse = s.nlse;
   f.ndelta = s.ndelta;
   f.pad = w.pad;
+  // Sequences of one key tile: surely none where all have Nk keys and those are more.
+  f.dq_first = kv_lens != nullptr || p->Nk <= kTile;
   f.dq = row_out(dq, p->B, p->H, p->Nq);
   f.dk = row_out(dk, p->B, p->Hk, p->Nk);
   f.dv = row_out(dv, p->B, p->Hk, p->Nk);

@@ -11,6 +11,11 @@
 // recomputed products cost 2/5 more tensor work than one kernel that would add its dQ tiles
 // into global memory in an order that changes from run to run.
 //
+// delta is taken from out as it was given, in bf16 and with P rounded. Over many keys that is no matter; of two keys'
+// gradients it would be half of the error (0.0054 instead of 0.0024 of their norm, in bf16). Where a
+// sequence's keys fit one tile, the dQ kernel has a row's P and dP at hand and forms delta = sum_j P dP
+// itself, for the dK / dV kernel too, which then runs after it.
+//
 // P and T are rounded to bf16 for the tensor cores (by at most 2^-8 of each value); S, dP,
 // delta, lse and every sum are fp32. Rows without keys have lse = -inf: their P is 0, and
 // delta is taken as 0.
@@ -28,7 +33,8 @@ constexpr int kBwdWarps = 16, kBwdThreads = 128 + 32 * kBwdWarps;
 struct AttendBwdArgs {
   AttendArgs p;
   const float* nlse;    // [B * H, pad] -lse2 (padding rows and rows without keys: -inf)
-  const float* ndelta;  // [B * H, pad] -delta
+  float* ndelta;        // [B * H, pad] -delta (written by the dQ kernel for sequences of one key tile)
+  int dq_first;         // the dQ kernel runs before the dK / dV kernel, and forms such deltas
   int pad;              // Nq rounded up to whole tiles
   RowOut dq, dk, dv;
   float* part;          // parts of units (see AttendWork): dQ [2 * CTAs][128][D], or [2 * CTAs][dK, dV][128][D]
@@ -287,7 +293,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
-  grid_dep_wait();
+  // Behind attend_dq_kernel this one needs its deltas, but only of sequences of one key tile; without such it runs
+  // beside that kernel where SMs are free (see there), and waits last.
+  bool late = false;
+  if (f.dq_first && a.lens) {
+    int one_tile = 0;
+    for (int b = tid; b < a.B; b += kBwdThreads) one_tile |= attend_len(a, b, false) <= kTile;
+    late = !__syncthreads_or(one_tile);
+  }
+  if (!late) grid_dep_wait();
   grid_dep_launch();
   const auto steps = [&](int u) { return dkv_unit(a, u, false).tiles * a.G; };
   AttendWork work = attend_work(a, steps, kBwdThreads);
@@ -468,6 +482,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
   }
+  if (late) grid_dep_wait();  // this kernel is not done before attend_dq_kernel is
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -511,9 +526,10 @@ __device__ __forceinline__ DqUnit dq_unit(const AttendArgs& a, int u, bool recor
 }
 
 struct DqItem {
-  int b, h, row0, len, lo, n, slot;
+  int b, h, row0, len, lo, n, slot, exact;  // exact: one key tile, delta is formed here
   __device__ __forceinline__ explicit DqItem(const AttendItem& i)
-      : b(i.v[0]), h(i.v[1]), row0(i.v[2]), len(i.v[3]), lo(i.v[4]), n(i.v[5]), slot(i.v[6]) {}
+      : b(i.v[0]), h(i.v[1]), row0(i.v[2]), len(i.v[3]), lo(i.v[4]), n(i.v[5]), slot(i.v[6]),
+        exact(i.v[7]) {}
   __device__ __forceinline__ bool stop() const { return b < 0; }
 };
 
@@ -535,6 +551,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   __shared__ uint64_t q_full, q_free, s_full[2], dp_full, dp_free, t_full[2], acc_full, acc_free, drain;
   __shared__ uint64_t k_full[ST], v_full[ST], k_free[ST], v_free[ST];
+  __shared__ uint64_t sum_full;
+  __shared__ float sums[2][4][kTile];  // a quarter's part of delta of each row; two buffers
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ ItemRing<kBwdWarps> items;
@@ -544,6 +562,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&q_full, 1);
     mbar_init(&q_free, 2);
     mbar_init(&dp_full, 1);
+    mbar_init(&sum_full, kBwdWarps);
     mbar_init(&dp_free, kBwdWarps);
     mbar_init(&acc_full, 1);
     mbar_init(&acc_free, 32 * kBwdWarps);
@@ -566,8 +585,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
-  // Runs beside attend_dkv_kernel where SMs are free: that kernel's CTAs let this one in after their own wait for
-  // attend_rows_kernel, whose results are all that this one needs of earlier kernels. The wait comes last.
+  // Behind attend_dkv_kernel this one runs beside it where SMs are free: that kernel's CTAs let this one in after
+  // their own wait for attend_rows_kernel, whose results are all that this one needs of earlier kernels.
+  // The wait then comes last.
+  if (f.dq_first) grid_dep_wait();
   grid_dep_launch();
   const auto steps = [&](int u) { return dq_unit(a, u, false).tiles; };
   AttendWork work = attend_work(a, steps, kBwdThreads);
@@ -584,7 +605,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       while (ok && work.next(a, steps, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
         const DqUnit w = dq_unit(a, u, true);
-        item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n)};
+        item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n),
+                f.dq_first && w.len <= kTile};
         ok = items.put(ni++, item, a.err, &abort_flag);
       }
       item.v[0] = -1;
@@ -714,7 +736,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sc = a.scale_log2;
     const uint64_t sc2 = f2_make(sc, sc);
-    uint32_t it = 0, nu = 0, ni = 0;
+    uint32_t it = 0, nu = 0, ni = 0, ne = 0;  // key tiles, units with work, items, exact units
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return warp_wait(bar, parity, a.err, &abort_flag);
@@ -728,7 +750,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int end = attend_key_end(a, w.len, row);
       const size_t at = (static_cast<size_t>(w.b) * a.H + w.h) * f.pad + row;
       const float nl = f.nlse[at], nd = f.ndelta[at];
-      const uint64_t nl2 = f2_make(nl, nl), nd2 = f2_make(nd, nd);
+      const uint64_t nl2 = f2_make(nl, nl);
+      uint64_t nd2 = f2_make(nd, nd);
       for (int j = 0; j < n; ++j, ++it) {
         const int key0 = (w.lo + j) * kTile + quarter * 32;
         const int upto = end - key0;  // columns of this quarter that the row sees
@@ -754,6 +777,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&dp_free);
         if (masked) keep_upto(d, upto, 0.f);  // dP of a key that is not there may be NaN
+        if (w.exact) {
+          uint64_t part = 0ull;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) part = f2_fma(pair_of(&p[e]), pair_of(&d[e]), part);
+          float(&buffer)[4][kTile] = sums[ne & 1];
+          buffer[quarter][r] = f2_lo(part) + f2_hi(part);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sum_full);
+          if (!(ok = wait(&sum_full, ne & 1))) break;
+          ++ne;
+          const float delta = (buffer[0][r] + buffer[1][r]) + (buffer[2][r] + buffer[3][r]);
+          nd2 = f2_make(-delta, -delta);
+          if (quarter == 0) f.ndelta[at] = -delta;
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const uint64_t y = f2_mul(f2_add(pair_of(&d[e]), nd2), pair_of(&p[e]));
@@ -797,7 +834,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
   }
-  grid_dep_wait();  // this kernel is not done before attend_dkv_kernel is
+  if (!f.dq_first) grid_dep_wait();  // this kernel is not done before attend_dkv_kernel is
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {

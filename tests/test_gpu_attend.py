@@ -167,6 +167,19 @@ def test_layouts_and_outputs(cuda_device):
     assert torch.equal(out, got[0])
 
 
+@pytest.mark.parametrize("Nq, Nk, lens", [(300, 2, None), (40, 3, None), (257, 128, None), (300, 700, [2, 1, 5])])
+@pytest.mark.parametrize("D", [128, 64])
+def test_gradients_of_few_keys(cuda_device, Nq, Nk, lens, D):
+    """delta of few keys is formed from P and dP, not from the rounded out. What is left are two roundings to bf16
+    (T, then the result), off by at most 2^-8 each and, evenly spread over a step of 2^-7 to 2^-8 of the
+    value, by less than 2^-8 / sqrt(3) in the mean square: less than 2^-8 sqrt(2 / 3) of the norm together."""
+    q, k, v, dO = _make(Nq + Nk, 3, 4, 2, Nq, Nk, D, cuda_device)
+    _, _, dq, dk, _ = _check(q, k, v, dO, lens)
+    refs = oa.gradients(q, k, v, dO, lens)
+    for got, ref in ((dq, refs[0]), (dk, refs[1])):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 * math.sqrt(2 / 3)
+
+
 def test_equal_calls_give_equal_bits(cuda_device):
     for Nq, Nk in ((1, 3000), (640, 640)):
         q, k, v, dO = _make(5, 2, 4, 2, Nq, Nk, 128, cuda_device)
