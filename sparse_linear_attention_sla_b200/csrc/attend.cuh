@@ -13,10 +13,10 @@
 // tensor cores (each p by at most 2^-8 of itself, independently; l sums the unrounded p);
 // S, acc, m and l are fp32. A row without keys gives out = 0 and lse = -inf.
 //
-// One persistent CTA per SM, 384 threads. A unit is, with more than 128 queries, 256 query rows
-// of one head (tiles A and B of 128 rows) that meet the same key tiles; with fewer ("narrow"),
-// one tile of as many (query head of the group, query) rows as fit, whose key tiles go to A and
-// B in turn, so that a single token of a group reads its keys once and both halves work:
+// One persistent CTA per SM, 384 threads. A tile is at most 128 rows, `heads` query heads that share a
+// key head x `tokens` queries. A unit is, with more than 128 queries, two neighbouring tiles A and B
+// that meet the same key tiles; with fewer ("narrow"), one tile whose key tiles go to A and B in
+// turn, so that a single token of a group reads its keys once and both halves work:
 //   warp 0       TMA: Q, then K_j and V_j tiles through a ring
 //   warps 1, 3   tcgen05 issuers of A and of B, on blocks t of 64 keys (half a tile):
 //                S_x = Q_x K_t^T, acc_x += P_x V_t
@@ -46,8 +46,8 @@ struct AttendSmem {
 
 struct AttendFwdArgs {
   AttendArgs p;
-  int narrow;        // Nq <= 128: units are one tile of `heads` x Nq rows
-  int heads;         // narrow: query heads of a tile, at most 128 / Nq
+  int narrow;        // Nq <= 128: units are one tile
+  int heads, tokens; // of a tile: `heads` query heads of a group x `tokens` queries, at most 128 rows
   int q_bytes;       // of one loaded Q tile
   RowOut out;
   float* lse;        // [B * H, Nq]
@@ -92,27 +92,18 @@ struct AttendItemView {
 __device__ __forceinline__ AttendUnit attend_unit(const AttendFwdArgs& f, int u, bool record) {
   const AttendArgs& a = f.p;
   AttendUnit w;
-  if (f.narrow) {
-    const int groups = (a.G + f.heads - 1) / f.heads;
-    w.b = u / groups / a.Hk;
-    w.hk = u / groups % a.Hk;
-    w.h = w.hk * a.G + u % groups * f.heads;
-    w.row0 = 0;
-    w.len = attend_len(a, w.b, record);
-    w.tiles[0] = w.tiles[1] = tiles_of(attend_key_end(a, w.len, a.Nq - 1));
-    return w;
-  }
-  const int pairs = (a.Nq + 2 * kTile - 1) / (2 * kTile);
-  const int bh = u / pairs;
-  w.b = bh / a.H;
-  w.h = bh % a.H;
-  w.hk = w.h / a.G;
-  w.row0 = u % pairs * 2 * kTile;
+  const int span = (f.narrow ? 1 : 2) * f.tokens;  // queries of a unit
+  const int spans = (a.Nq + span - 1) / span, groups = (a.G + f.heads - 1) / f.heads;
+  const int g = u / spans;
+  w.row0 = u % spans * span;
+  w.b = g / groups / a.Hk;
+  w.hk = g / groups % a.Hk;
+  w.h = w.hk * a.G + g % groups * f.heads;
   w.len = attend_len(a, w.b, record);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int r = w.row0 + x * kTile;
-    w.tiles[x] = r < a.Nq ? tiles_of(attend_key_end(a, w.len, min(r + kTile, a.Nq) - 1)) : 0;
+    const int r = w.row0 + (f.narrow ? 0 : x * f.tokens);
+    w.tiles[x] = r < a.Nq ? tiles_of(attend_key_end(a, w.len, min(r + f.tokens, a.Nq) - 1)) : 0;
   }
   return w;
 }
@@ -120,14 +111,10 @@ __device__ __forceinline__ AttendUnit attend_unit(const AttendFwdArgs& f, int u,
 // The head and query of row r of the unit's tile x; false where the row is none.
 template <class Unit>
 __device__ __forceinline__ bool attend_row(const AttendFwdArgs& f, const Unit& w, int x, int r, int& h, int& i) {
-  if (f.narrow) {
-    h = w.h + r / f.p.Nq;
-    i = r % f.p.Nq;
-    return r < f.heads * f.p.Nq && h < (w.hk + 1) * f.p.G;
-  }
-  h = w.h;
-  i = w.row0 + x * kTile + r;
-  return i < f.p.Nq;
+  const int k = f.heads == 1 ? 0 : r / f.tokens, t = r - k * f.tokens;
+  h = w.h + k;
+  i = w.row0 + (f.narrow ? 0 : x * f.tokens) + t;
+  return k < f.heads && t < f.tokens && h < (w.hk + 1) * f.p.G && i < f.p.Nq;
 }
 
 // Keys of 32 columns from key0 on that a row does not see (its keys end at `end`) take -inf.
@@ -201,9 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ni = 0;
       int u, lo, hi, n, to;
       bool ok = true;
-      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+      AttendUnit w;  // the unit that `next` looked at last, which is the one it gives
+      const auto look = [&](int v) {
+        w = attend_unit(f, v, true);
+        return w.steps(narrow);
+      };
+      while (ok && work.next(a, look, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
-        const AttendUnit w = attend_unit(f, u, true);
         item = {w.b, w.h, w.hk, w.row0, w.len, lo, w.count(narrow, 0, lo, hi), w.count(narrow, 1, lo, hi),
                 part_slot(lo, hi, n)};
         ok = items.put(ni++, item, a.err, &abort_flag);
@@ -241,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&q_full, q_tiles * f.q_bytes);
           for (int x = 0; x < q_tiles; ++x)
             for (int b = 0; b < DB; ++b)
-              tma_load_5d(sQ + x * L::TILE + b * kBox, &map_q, &q_full, b * 64, w.row0 + x * kTile, w.h % a.G, w.hk,
+              tma_load_5d(sQ + x * L::TILE + b * kBox, &map_q, &q_full, b * 64, w.row0 + x * f.tokens, w.h % a.G, w.hk,
                           w.b);
           ++nq;
         }
@@ -373,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool real = attend_row(f, w, x, r, h, i);
       const int n = w.blocks(x), other = w.blocks(x ^ 1);
       const int end = attend_key_end(a, w.len, i);                                    // this row's keys
-      const int end_min = attend_key_end(a, w.len, narrow ? 0 : w.row0 + x * kTile);  // fewest of a row
+      const int end_min = attend_key_end(a, w.len, w.row0 + (narrow ? 0 : x * f.tokens));  // fewest of a row
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < n; ++t, ++ns) {
         const uint32_t b = ns & 1, sb = s_addr + b * 64;

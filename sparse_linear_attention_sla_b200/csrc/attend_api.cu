@@ -57,7 +57,7 @@ Share share_out(long long units, long long steps, bool uniform) {
 struct AttendPlan {
   sla_attend_problem p;
   int pad;             // Nq rounded up to whole tiles
-  int narrow, heads;   // forward: see AttendFwdArgs
+  int narrow, heads, tokens;  // forward: see AttendFwdArgs
   Share fwd, dkv, dq;
 };
 
@@ -79,7 +79,7 @@ sla_status make_plan(const sla_attend_problem* p, bool has_lens, AttendPlan* w) 
   if (!std::isfinite(p->scale) || !(p->scale > 0.f)) return fail(SLA_ERR_INVALID_ARG, "scale must be finite and > 0");
   if (p->Nq > (1 << 24) || p->Nk > (1 << 24)) return fail(SLA_ERR_UNSUPPORTED, "Nq, Nk must be at most 2^24");
   const long long BH = static_cast<long long>(p->B) * p->H, BHk = static_cast<long long>(p->B) * p->Hk;
-  const long long qt = (p->Nq + kTile - 1) / kTile, kt = (p->Nk + kTile - 1) / kTile, pairs = (qt + 1) / 2;
+  const long long qt = (p->Nq + kTile - 1) / kTile, kt = (p->Nk + kTile - 1) / kTile;
   if (BH * qt >= (1ll << 28) || BHk * kt >= (1ll << 28)) return fail(SLA_ERR_UNSUPPORTED, "B*H*N too large");
   const long long group = p->H / p->Hk;
   if (group * qt >= (1ll << 30)) return fail(SLA_ERR_UNSUPPORTED, "H / Hk * Nq too large");
@@ -88,13 +88,25 @@ sla_status make_plan(const sla_attend_problem* p, bool has_lens, AttendPlan* w) 
   const bool uniform = !p->causal && !has_lens;
   w->narrow = p->Nq <= kTile;
   w->heads = 1;
-  if (w->narrow) {
-    w->heads = static_cast<int>(group < kTile / p->Nq ? group : kTile / p->Nq);
-    // one query tile sees the same keys whatever the mask
-    w->fwd = share_out(BHk * ((group + w->heads - 1) / w->heads), (kt + 1) / 2, !has_lens);
-  } else {
-    w->fwd = share_out(BH * pairs, kt, uniform);
+  w->tokens = w->narrow ? p->Nq : kTile;
+  // Tiles of more heads and fewer queries: as few tiles as can be (130 queries of a group of 3: 4 tiles instead of
+  // 6), and of equally many the one of fewest queries where the mask is causal, whose diagonal is then
+  // cut more finely.
+  long long tiles = group * ((p->Nq + w->tokens - 1) / w->tokens);
+  for (int h = 2; h <= group && h <= kTile; ++h) {
+    const int t = p->Nq < kTile / h ? p->Nq : kTile / h;
+    const long long n = (group + h - 1) / h * ((p->Nq + t - 1) / t);
+    if (n < tiles || (n == tiles && p->causal && !w->narrow)) {
+      if (w->narrow && t < p->Nq) continue;  // one tile of a group holds all queries
+      tiles = n;
+      w->heads = h;
+      w->tokens = t;
+    }
   }
+  const long long span = (w->narrow ? 1 : 2) * w->tokens, spans = (p->Nq + span - 1) / span;
+  const long long fwd_units = BHk * ((group + w->heads - 1) / w->heads) * spans;
+  // one tile sees the same keys whatever the mask
+  w->fwd = share_out(fwd_units, w->narrow ? (kt + 1) / 2 : kt, w->narrow ? !has_lens : uniform);
   w->dkv = share_out(BHk * kt, group * qt, uniform);
   w->dq = share_out(BH * qt, kt, uniform);
   return SLA_OK;
@@ -292,15 +304,15 @@ sla_status sla_attend(const sla_attend_problem* p, const sla_tensor* q, const sl
   AttendSpace s;
   SLA_TRY(check_space(w, ws, ws_bytes, false, &s));
   Maps m;
-  const int tokens = w.narrow ? p->Nq : kTile;
-  SLA_TRY(query_map(&m.q, q, *p, tokens, w.heads));
+  SLA_TRY(query_map(&m.q, q, *p, w.tokens, w.heads));
   SLA_TRY(operand_map(&m.k, k, p->B, p->Hk, p->Nk, p->D));
   SLA_TRY(operand_map(&m.v, v, p->B, p->Hk, p->Nk, p->D));
   AttendFwdArgs f{};
   f.p = common_args(w, kv_lens, s.err, w.fwd, s.meta);
   f.narrow = w.narrow;
   f.heads = w.heads;
-  f.q_bytes = tokens * w.heads * p->D * 2;
+  f.tokens = w.tokens;
+  f.q_bytes = w.tokens * w.heads * p->D * 2;
   f.out = row_out(out, p->B, p->H, p->Nq);
   f.lse = lse;
   f.part = s.part;

@@ -315,9 +315,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t ni = 0;
       int u, lo, hi, n, to;
       bool ok = true;
-      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+      DkvUnit w;  // the unit that `next` looked at last, which is the one it gives
+      const auto look = [&](int v) {
+        w = dkv_unit(a, v, true);
+        return w.tiles * a.G;
+      };
+      while (ok && work.next(a, look, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
-        const DkvUnit w = dkv_unit(a, u, true);
         item = {w.b, w.hk, w.key0, w.len, w.first, w.tiles, w.dead, lo, hi, part_slot(lo, hi, n)};
         ok = items.put(ni++, item, a.err, &sh.abort_flag);
       }
@@ -602,9 +606,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t ni = 0;
       int u, lo, hi, n, to;
       bool ok = true;
-      while (ok && work.next(a, steps, u, lo, hi, n, to)) {
+      DqUnit w;  // the unit that `next` looked at last, which is the one it gives
+      const auto look = [&](int v) {
+        w = dq_unit(a, v, true);
+        return w.tiles;
+      };
+      while (ok && work.next(a, look, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
-        const DqUnit w = dq_unit(a, u, true);
         item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n),
                 f.dq_first && w.len <= kTile};
         ok = items.put(ni++, item, a.err, &abort_flag);

@@ -26,9 +26,9 @@ struct AttendArgs {
 
 // Blocks of three warpgroups: the first holds the TMA and the MMA warp, the other two the warps
 // that compute. 384 threads are launched with 168 registers each (64512); the first warpgroup
-// keeps 88 and the others take 208: 128 * (88 + 2 * 208) = 64512.
+// keeps 72 and the others take 216: 128 * (72 + 2 * 216) = 64512.
 constexpr int kThreads = 384;
-constexpr int kIssueRegs = 88, kComputeRegs = 208;
+constexpr int kIssueRegs = 72, kComputeRegs = 216;
 static_assert(128 * (kIssueRegs + 2 * kComputeRegs) <= kThreads * 168, "more registers than the block has");
 
 // The first warpgroup's warps. Two issue MMAs, each its own chain of products: what one warp needs to

@@ -74,6 +74,8 @@ SHAPES = [
     (1, 24, 2, 11, 700),    # twelve heads of a group: eleven in one tile, one in the next
     (1, 3, 3, 128, 777),    # the most queries of one tile
     (40, 4, 2, 130, 130),   # more units than SMs
+    (2, 6, 2, 130, 700),    # tiles of three heads and 42 queries
+    (1, 10, 2, 200, 333),   # tiles of five heads and 25 queries where that makes fewest, or equally many and causal
 ]
 
 
