@@ -182,6 +182,21 @@ def test_gradients_of_few_keys(cuda_device, Nq, Nk, lens, D):
         assert float((got.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 * math.sqrt(2 / 3)
 
 
+def test_nan_gradients_stay_out_of_rows_without_a_part(cuda_device):
+    """NaN in dO spreads to what it enters; keys behind a length and queries without keys get exact zeros."""
+    for Nq, Nk, n, causal in ((40, 300, 130, False), (300, 200, 60, True)):
+        q, k, v, dO = _make(1, 1, 4, 2, Nq, Nk, 128, cuda_device)
+        lens = torch.tensor([n], dtype=torch.int32, device=cuda_device)
+        out, lse = binding.attend(q, k, v, lens, causal=causal)
+        dO = torch.full_like(dO, math.nan)
+        k[:, :, n - 1] = math.nan  # a key of the sequence
+        dq, dk, dv = binding.attend_backward(q, k, v, out, lse, dO, lens, causal=causal)
+        assert (dk[:, :, n:] == 0).all() and (dv[:, :, n:] == 0).all()
+        dead = max(0, Nq - n) if causal else 0
+        assert (dq[:, :, :dead] == 0).all() and dq[:, :, dead:].isnan().all()
+        assert dv[:, :, :n].isnan().all()
+
+
 def test_equal_calls_give_equal_bits(cuda_device):
     for Nq, Nk in ((1, 3000), (640, 640)):
         q, k, v, dO = _make(5, 2, 4, 2, Nq, Nk, 128, cuda_device)
@@ -294,6 +309,10 @@ def test_refusals(cuda_device):
         lambda: binding.attend(q[:, :, :0], k, v),
         lambda: binding.attend(q.transpose(2, 3).contiguous().transpose(2, 3), k, v),
         lambda: binding.attend(q, k, v, ws=torch.empty(64, dtype=torch.uint8, device=cuda_device)),
+        lambda: binding.attend(q, k, v, ws=torch.empty(1 << 24, dtype=torch.uint8)),                           # on the host
+        lambda: binding.attend(q, k, v, ws=torch.empty(1 << 22, dtype=torch.float32, device=cuda_device)),
+        lambda: binding.attend_backward(q, k, v, out, lse, dO, ws=torch.empty(1 << 24, dtype=torch.uint8)),
+        lambda: binding.attend(q, k, v, out=q),
         lambda: binding.attend_backward(q, k, v, out, lse.double(), dO),
         lambda: binding.attend_backward(q, k, v, out, lse, dO[:, :, 1:]),
     ]
