@@ -356,7 +356,7 @@ sla_status sla_route_noalloc(const sla_problem* p, const void* q, const void* k,
  *
  * A head's first channels are cut into one run of channels[a] channels per axis a; channels
  * behind the last run are copied. Pair i of axis a at a token with position p_a turns by
- *     phi = p_a * base^(-2 i / channels[a])          (formed in fp64)
+ *     phi = p_a * base^(-2 i / channels[a])          (a 64-bit fraction of a turn)
  *     y1 = x1 cos(phi) - x2 sin(phi),  y2 = x2 cos(phi) + x1 sin(phi)   (fp32, rounded once)
  */
 
@@ -384,7 +384,7 @@ typedef struct {
 } sla_rotary_spec;
 
 /* Rotate q [B, Hq, N, D] and k [B, Hk, N, D] (one of Hq, Hk may be 0; its tensors are then not
- * read) into q_out and k_out. D is 64 or 128; B at most 65535. An output may be its own input
+ * read) into q_out and k_out. D is 64 or 128; B at most 65535, N at most 2^30. An output may be its own input
  * (the same pointer and strides), else the two must not overlap. One launch on `stream`.
  * Returns SLA_ERR_INVALID_ARG / SLA_ERR_UNSUPPORTED on bad arguments (nothing enqueued),
  * SLA_ERR_CUDA if the launch fails, else SLA_OK. */

@@ -534,6 +534,8 @@ def rotary_spec(axes, grid=None, positions=None, start=None, base=10000.0, pairi
     halves of an axis' channels.
     """
     axes = tuple(int(a) for a in axes)
+    if any(not -2 ** 31 <= int(x) < 2 ** 31 for x in (*axes, *(grid or ()), *(start or ()))):
+        raise ValueError("channels, grid and start must fit 32 bits")
     if not 1 <= len(axes) <= 4:
         raise ValueError(f"one to four axes, got {len(axes)}")
     if (grid is None) == (positions is None):
@@ -609,13 +611,37 @@ def _span(t):
     return first, first + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
+def _check_apart(name, y, *others):
+    """The output y shares no memory with the other tensors. Heads or tokens of one buffer that lie between
+    each other's rows are apart where neither's rows reach into the other's."""
+    c, d = _span(y)
+    for x in others:
+        a, b = _span(x)
+        if a < d and c < b and not _interleaved(x, y):
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def _interleaved(x, y):
+    """x and y are slices of one buffer that never meet: every step between rows is a multiple of the smallest, and
+    within that one their row blocks lie apart."""
+    steps = [s * t.element_size() for t in (x, y) for n, s in zip(t.shape[:3], t.stride()) if n > 1]
+    for period in sorted(set(steps)):
+        def block(t):  # bytes of the dimensions that stay within the period
+            return (sum((n - 1) * s for n, s in zip(t.shape, t.stride()) if s * t.element_size() < period) + 1) \
+                * t.element_size()
+        if any(s % period and s > period for s in steps):
+            continue
+        gap = (y.data_ptr() - x.data_ptr()) % period
+        if block(x) <= gap and block(y) <= period - gap:
+            return True
+    return False
+
+
 def _check_in_place(name, x, y):
     """y is x itself, or apart from it: tensors that share part of their memory cannot be rotated."""
     if y.data_ptr() == x.data_ptr() and y.stride() == x.stride() and y.dtype == x.dtype:
         return
-    (a, b), (c, d) = _span(x), _span(y)
-    if a < d and c < b:
-        raise ValueError(f"{name} overlaps its input without being the same tensor")
+    _check_apart(name, y, x)
 
 
 def _rotary_call(q, k, spec, out, dtype, names, backward):
@@ -648,6 +674,9 @@ def _rotary_call(q, k, spec, out, dtype, names, backward):
             args[2 * w + 1] = _check_heads(f"out of {names[w]}", y, B, H, N, D, dtype, dev)
             _check_in_place(f"out of {names[w]}", x, y)
             outs[w] = y
+    if out is not None and args[0] is not None and args[2] is not None:  # one's output may not be the other's
+        _check_apart(f"out of {names[0]}", outs[0], k, outs[1])
+        _check_apart(f"out of {names[1]}", outs[1], q)
     lib, call = load_library(), _Call(dev)
     in_code, out_code = int(in_dtype is torch.float32), int(dtype is torch.float32)  # SLA_BF16, SLA_F32
     if backward:
@@ -697,6 +726,12 @@ def _attend_space(p, device, backward):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _given_space(ws, dev):
+    if not isinstance(ws, torch.Tensor) or ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a workspace of new_workspace_attend on {dev}")
+    return ws
+
+
 def _attend_inputs(q, k, v, kv_lens, causal, scale):
     p = attend_problem(q, k, causal, scale)
     dev, bf16 = q.device, torch.bfloat16
@@ -721,9 +756,9 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
         out, o = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
     else:
         o = _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+        _check_apart("out", out, q, k, v)
     lse = q.new_empty((p.B, p.H, p.Nq), dtype=torch.float32)
-    if ws is None:
-        ws = _attend_space(p, dev, False)
+    ws = _attend_space(p, dev, False) if ws is None else _given_space(ws, dev)
     _Call(dev)(load_library().sla_attend, p, *args, _address(kv_lens), o, lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
 
@@ -740,8 +775,7 @@ def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=Non
     dq, a = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
     dk, b = _new_heads(k, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
     dv, c = _new_heads(v, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
-    if ws is None:
-        ws = _attend_space(p, dev, True)
+    ws = _attend_space(p, dev, True) if ws is None else _given_space(ws, dev)
     _Call(dev)(load_library().sla_attend_backward, p, *args, o, lse.data_ptr(), g, _address(kv_lens), a, b, c,
                ws.data_ptr(), ws.numel())
     return dq, dk, dv

@@ -55,6 +55,7 @@ sla_status rotate(const sla_rotary_spec* spec, const RotaryCall& c, int in_type,
   if (c.B < 1 || c.N < 1 || c.heads[0] < 0 || c.heads[1] < 0 || c.heads[0] + static_cast<long long>(c.heads[1]) < 1)
     return fail(SLA_ERR_INVALID_ARG, "B, N and Hq + Hk must be >= 1");
   if (c.D != 64 && c.D != 128) return fail(SLA_ERR_UNSUPPORTED, "D=%d not supported (64 or 128)", c.D);
+  if (c.N > (1 << 30)) return fail(SLA_ERR_UNSUPPORTED, "N=%d exceeds 2^30", c.N);  // token indices stay in 32 bits
   if (c.B > 65535) return fail(SLA_ERR_UNSUPPORTED, "B=%d exceeds 65535", c.B);
   if (static_cast<long long>(c.heads[0]) + c.heads[1] > INT_MAX / 2)
     return fail(SLA_ERR_UNSUPPORTED, "Hq + Hk too large");

@@ -1,6 +1,6 @@
 """GPU parity of the rotary positions against the fp64 oracle.
 
-A value is formed in fp32 from an angle that is reduced in fp64: cos and sin are off by at most
+A value is formed in fp32 from an angle that is reduced in 64 bits: cos and sin are off by at most
 2^-22 (their argument, at most pi, is rounded to fp32 by 2^-23, and sincosf by 2 steps), the two
 products and their sum by 2^-24 each, so |error| <= 2^-21 (|x1| + |x2|), plus half a bf16 step
 (2^-8 of the value) where the result is bf16.
@@ -129,6 +129,19 @@ def test_captured_and_replayed(cuda_device):
     assert torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
+def test_in_place_within_one_projection(cuda_device):
+    """q and k as slices of one [B, N, 3, H, D] buffer, turned where they lie; v between them stays as it was."""
+    buf = torch.randn(2, 50, 3, 4, 64, device=cuda_device, generator=torch.Generator(cuda_device).manual_seed(8))
+    buf = buf.to(torch.bfloat16)
+    q, v, k = (buf[:, :, i].transpose(1, 2) for i in range(3))
+    spec = binding.rotary_spec((32, 32), grid=(5, 10))
+    want, kept = binding.rotary(q, k, spec), v.clone()
+    binding.rotary(q, k, spec, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept)
+    with pytest.raises(ValueError):
+        binding.rotary(q, k, spec, out=(q, buf[:, :, 1:].flatten(2, 3)[:, :, 2:6].transpose(1, 2)))  # half of v, half of k
+
+
 def test_refusals(cuda_device):
     x = _make(1, 1, 2, 10, 64, torch.bfloat16, cuda_device)
     ok = binding.rotary_spec((64,), grid=(10,))
@@ -152,6 +165,9 @@ def test_refusals(cuda_device):
         lambda: binding.rotary_backward(x, None, ok, dtype=torch.float32),
         lambda: binding.rotary(x[:, :, 1:], None, binding.rotary_spec((64,), grid=(9,)), out=(x[:, :, :9], None)),
         lambda: binding.rotary(x.cpu(), None, ok),
+        lambda: binding.rotary(x, x.clone(), ok, out=(x, x)),
+        lambda: binding.rotary_spec((64,), grid=(2 ** 32 + 10,)),
+        lambda: binding.rotary_spec((64,), grid=(10,), start=(2 ** 31,)),
     ]
     for f in bad:
         with pytest.raises((ValueError, binding.SlaError)):
