@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -66,6 +67,10 @@ class RotarySpec(ctypes.Structure):
                 ("start", ctypes.c_int * 4), ("positions", ctypes.c_void_p), ("positions_stride_b", ctypes.c_int64),
                 ("pairing", ctypes.c_int), ("base", ctypes.c_double)]
     positions_tensor = None
+
+
+_ROTARY_SPEC = struct.Struct("@13iPqid")  # RotarySpec's fields, in C's own alignment
+assert _ROTARY_SPEC.size == ctypes.sizeof(RotarySpec)
 
 
 class AttendProblem(ctypes.Structure):
@@ -533,32 +538,33 @@ def rotary_spec(axes, grid=None, positions=None, start=None, base=10000.0, pairi
     int32 tensor [N, len(axes)] or [B, N, len(axes)]. pairing: 0 neighbouring channels, 1 the two
     halves of an axis' channels.
     """
-    axes = tuple(int(a) for a in axes)
-    if any(not -2 ** 31 <= int(x) < 2 ** 31 for x in (*axes, *(grid or ()), *(start or ()))):
-        raise ValueError("channels, grid and start must fit 32 bits")
-    if not 1 <= len(axes) <= 4:
-        raise ValueError(f"one to four axes, got {len(axes)}")
+    axes = tuple(map(int, axes))
+    n = len(axes)
+    if not 1 <= n <= 4:
+        raise ValueError(f"one to four axes, got {n}")
     if (grid is None) == (positions is None):
         raise ValueError("give either grid or positions")
-    spec = RotarySpec(n_axes=len(axes), pairing=int(pairing), base=float(base))
-    for a, d in enumerate(axes):
-        spec.channels[a] = d
     if grid is not None:
-        grid = tuple(int(g) for g in grid)
-        start = tuple(int(x) for x in start) if start is not None else (0,) * len(axes)
-        if len(grid) != len(axes) or len(start) != len(axes):
-            raise ValueError(f"grid and start need one entry per axis ({len(axes)})")
-        for a in range(len(axes)):
-            spec.grid[a], spec.start[a] = grid[a], start[a]
+        grid = tuple(map(int, grid))
+        start = tuple(map(int, start)) if start is not None else (0,) * n
+        if len(grid) != n or len(start) != n:
+            raise ValueError(f"grid and start need one entry per axis ({n})")
+        where, stride = 0, 0
     else:
         if start is not None:
             raise ValueError("start goes with grid")
         if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32 \
-                or positions.dim() not in (2, 3) or positions.shape[-1] != len(axes) or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 CUDA tensor [N, {len(axes)}] or [B, N, {len(axes)}]")
-        spec.positions = positions.data_ptr()
-        spec.positions_stride_b = positions.shape[-2] * len(axes) if positions.dim() == 3 else 0
-        spec.positions_tensor = positions
+                or positions.dim() not in (2, 3) or positions.shape[-1] != n or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 CUDA tensor [N, {n}] or [B, N, {n}]")
+        grid = start = (0,) * n
+        where, stride = positions.data_ptr(), positions.shape[-2] * n if positions.dim() == 3 else 0
+    none = (0,) * (4 - n)
+    try:  # packed in one step: filling the structure field by field takes longer than the kernel's launch
+        spec = RotarySpec.from_buffer_copy(_ROTARY_SPEC.pack(n, *axes, *none, *grid, *none, *start, *none, where, stride,
+                                                             int(pairing), float(base)))
+    except struct.error as e:
+        raise ValueError(f"channels, grid, start and pairing must fit 32 bits: {e}") from None
+    spec.positions_tensor = positions
     return spec
 
 
@@ -578,8 +584,8 @@ def _check_heads(name, t, B, H, N, D, dtype, device):
 
 def _new_heads(like, B, H, N, D, dtype):
     """A contiguous [B, H, N, D] tensor on `like`'s device, and as the library takes it."""
-    t = like.new_empty((B, H, N, D), dtype=dtype)
     n = N * D
+    t = torch.empty_strided((B, H, N, D), (H * n, n, D, 1), dtype=dtype, device=like.device)
     return t, Tensor(t.data_ptr(), H * n, n, D)
 
 
