@@ -573,19 +573,19 @@ def _check_heads(name, t, B, H, N, D, dtype, device):
     the library takes it."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype or t.shape != (B, H, N, D) or t.stride(3) != 1:
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != (B, H, N, D) or strides[3] != 1:
         raise ValueError(f"{name} must be {dtype} of shape {(B, H, N, D)} with contiguous channels, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+                         f"{tuple(t.shape)} with strides {strides}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    b, h, n, _ = t.stride()
-    return Tensor(t.data_ptr(), b, h, n)
+    return Tensor(t.data_ptr(), strides[0], strides[1], strides[2])
 
 
-def _new_heads(like, B, H, N, D, dtype):
-    """A contiguous [B, H, N, D] tensor on `like`'s device, and as the library takes it."""
+def _new_heads(device, B, H, N, D, dtype):
+    """A contiguous [B, H, N, D] tensor, and as the library takes it."""
     n = N * D
-    t = torch.empty_strided((B, H, N, D), (H * n, n, D, 1), dtype=dtype, device=like.device)
+    t = torch.empty_strided((B, H, N, D), (H * n, n, D, 1), dtype=dtype, device=device)
     return t, Tensor(t.data_ptr(), H * n, n, D)
 
 
@@ -602,7 +602,7 @@ class _Call:
         self.stream = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __call__(self, f, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if torch._C._cuda_getDevice() == self.device.index:
             status = f(*args, self.stream)
         else:
             with torch.cuda.device(self.device):
@@ -659,6 +659,8 @@ def _rotary_call(q, k, spec, out, dtype, names, backward):
     if not isinstance(first, torch.Tensor) or first.dim() != 4:
         raise ValueError(f"{names[0]} and {names[1]} must be [B, H, N, D] tensors")
     (B, _, N, D), dev, in_dtype = first.shape, first.device, first.dtype
+    if max(first.shape) >= 2 ** 31:
+        raise ValueError(f"sizes must fit 32 bits, got {tuple(first.shape)}")
     if in_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{names[0]} and {names[1]} must be bf16 or fp32, got {in_dtype}")
     dtype = in_dtype if dtype is None else dtype
@@ -675,7 +677,7 @@ def _rotary_call(q, k, spec, out, dtype, names, backward):
         args[2 * w] = _check_heads(names[w], x, B, H, N, D, in_dtype, dev)
         y = out[w] if out is not None else None
         if y is None:
-            outs[w], args[2 * w + 1] = _new_heads(x, B, H, N, D, dtype)
+            outs[w], args[2 * w + 1] = _new_heads(dev, B, H, N, D, dtype)
         else:
             args[2 * w + 1] = _check_heads(f"out of {names[w]}", y, B, H, N, D, dtype, dev)
             _check_in_place(f"out of {names[w]}", x, y)
@@ -713,8 +715,11 @@ def attend_problem(q, k, causal=False, scale=None) -> AttendProblem:
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, H, N, D] tensors")
     B, H, Nq, D = q.shape
+    _, Hk, Nk, _ = k.shape
+    if max(B, H, Nq, Hk, Nk, D) >= 2 ** 31:
+        raise ValueError(f"sizes must fit 32 bits, got {tuple(q.shape)} and {tuple(k.shape)}")
     scale = float(scale) if scale is not None else max(D, 1) ** -0.5
-    return AttendProblem(B, H, k.shape[1], Nq, k.shape[2], D, int(bool(causal)), scale)
+    return AttendProblem(B, H, Hk, Nq, Nk, D, int(bool(causal)), scale)
 
 
 def new_workspace_attend(p: AttendProblem, device, backward: bool = False) -> torch.Tensor:
@@ -740,14 +745,15 @@ def _given_space(ws, dev):
 
 def _attend_inputs(q, k, v, kv_lens, causal, scale):
     p = attend_problem(q, k, causal, scale)
+    (B, H, Nq, D), (_, Hk, Nk, _) = q.shape, k.shape
     dev, bf16 = q.device, torch.bfloat16
-    args = (_check_heads("q", q, p.B, p.H, p.Nq, p.D, bf16, dev), _check_heads("k", k, p.B, p.Hk, p.Nk, p.D, bf16, dev),
-            _check_heads("v", v, p.B, p.Hk, p.Nk, p.D, bf16, dev))
+    args = (_check_heads("q", q, B, H, Nq, D, bf16, dev), _check_heads("k", k, B, Hk, Nk, D, bf16, dev),
+            _check_heads("v", v, B, Hk, Nk, D, bf16, dev))
     if kv_lens is not None and (not isinstance(kv_lens, torch.Tensor) or kv_lens.dtype != torch.int32
-                                or tuple(kv_lens.shape) != (p.B,) or not kv_lens.is_contiguous()
+                                or tuple(kv_lens.shape) != (B,) or not kv_lens.is_contiguous()
                                 or kv_lens.device != dev):
-        raise ValueError(f"kv_lens must be contiguous int32 [{p.B}] on {dev}")
-    return p, dev, args
+        raise ValueError(f"kv_lens must be contiguous int32 [{B}] on {dev}")
+    return p, (B, H, Hk, Nq, Nk, D), dev, args
 
 
 def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
@@ -757,13 +763,13 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
     divides H. kv_lens: int32 [B] keys of each sequence (None: Nk). causal: query i sees the keys
     j <= i + len - Nq. scale: 1 / sqrt(D) if None. A query without keys gives 0 and lse = -inf.
     ws: new_workspace_attend's, kept where a device-side error is to be asked for with check(ws)."""
-    p, dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    p, (B, H, Hk, Nq, Nk, D), dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
     if out is None:
-        out, o = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
+        out, o = _new_heads(dev, B, H, Nq, D, torch.bfloat16)
     else:
-        o = _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
+        o = _check_heads("out", out, B, H, Nq, D, torch.bfloat16, dev)
         _check_apart("out", out, q, k, v)
-    lse = q.new_empty((p.B, p.H, p.Nq), dtype=torch.float32)
+    lse = q.new_empty((B, H, Nq), dtype=torch.float32)
     ws = _attend_space(p, dev, False) if ws is None else _given_space(ws, dev)
     _Call(dev)(load_library().sla_attend, p, *args, _address(kv_lens), o, lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
@@ -772,15 +778,15 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
 def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=None, ws=None):
     """sla_attend_backward: (dq [B,H,Nq,D], dk, dv [B,Hk,Nk,D]) bf16 of sum(dO * out), from attend's
     out and lse of the same arguments. Equal calls give equal bits."""
-    p, dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
-    o = _check_heads("out", out, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    g = _check_heads("dO", dO, p.B, p.H, p.Nq, p.D, torch.bfloat16, dev)
-    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.shape != (p.B, p.H, p.Nq) \
+    p, (B, H, Hk, Nq, Nk, D), dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
+    o = _check_heads("out", out, B, H, Nq, D, torch.bfloat16, dev)
+    g = _check_heads("dO", dO, B, H, Nq, D, torch.bfloat16, dev)
+    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.shape != (B, H, Nq) \
             or not lse.is_contiguous() or lse.device != dev:
-        raise ValueError(f"lse must be contiguous fp32 [{p.B}, {p.H}, {p.Nq}] on {dev}")
-    dq, a = _new_heads(q, p.B, p.H, p.Nq, p.D, torch.bfloat16)
-    dk, b = _new_heads(k, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
-    dv, c = _new_heads(v, p.B, p.Hk, p.Nk, p.D, torch.bfloat16)
+        raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on {dev}")
+    dq, a = _new_heads(dev, B, H, Nq, D, torch.bfloat16)
+    dk, b = _new_heads(dev, B, Hk, Nk, D, torch.bfloat16)
+    dv, c = _new_heads(dev, B, Hk, Nk, D, torch.bfloat16)
     ws = _attend_space(p, dev, True) if ws is None else _given_space(ws, dev)
     _Call(dev)(load_library().sla_attend_backward, p, *args, o, lse.data_ptr(), g, _address(kv_lens), a, b, c,
                ws.data_ptr(), ws.numel())
