@@ -13,10 +13,9 @@
 // Bound by HBM: every element is read once and written once. A thread keeps one 8-channel
 // chunk of one token through all heads of q and k that its block takes, so the angles are formed
 // once per token and not once per head. They are 64-bit fractions of a turn (see rotary_kernel): an
-// fp32 angle at position 1e6 would be off by 0.06, and fp64 sines cost more than the copy (a block
-// per four heads, which forms them six times as often as eight blocks to an SM do, lost on every size).
-// Measured: 32760 tokens, 12 + 12 heads of 128 channels, bf16: 72.8 us, 5.5 TB/s of 6.5 measured for a
-// plain copy (fp64 angles 83); fp32 gradients to bf16 98.3 us, 6.1 TB/s.
+// fp32 angle at position 1e6 would be off by 0.06, and sines of fp64 angles cost more.
+// Measured: 32760 tokens, 12 + 12 heads of 128 channels, bf16: 73 us, 5.5 TB/s of 6.5 measured for a
+// plain copy (fp64 angles 83); fp32 gradients to bf16 98 us, 6.1 TB/s.
 #pragma once
 
 #include <climits>

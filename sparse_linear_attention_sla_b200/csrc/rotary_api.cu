@@ -30,9 +30,12 @@ sla_status launch(RotaryArgs& a, int B, cudaStream_t st) {
   constexpr int tokens = sla::kRotaryThreads / (D / 8);
   const long long nx = (a.N + tokens - 1) / tokens;
   const int total = a.heads[0] + a.heads[1];
-  // A block takes as many heads as leave eight blocks for every SM, in steps of the unrolled
-  // loop where there are enough.
-  long long per = total * nx * B / (8ll * sm_count());
+  // A block forms its tokens' angles once for all heads that it takes, which costs about as much as six heads do: it
+  // takes as many as leave one and a half blocks for every SM, in steps of the unrolled loop where there are
+  // enough. (One head to a block, four, this rule: 2 x 4093 tokens of 16 + 4 heads of 64 channels 47.6, 17.1,
+  // 12.2 us; 2040 tokens of 24 heads of 128: 21.1, 8.9, 6.6, and 8.1 with all 24; 1500 tokens of 48 heads of 64:
+  // 13.4, 5.6, 5.1, and 7.4 with 24.)
+  long long per = total * nx * B * 2 / (3ll * sm_count());
   per = per < 1 ? 1 : per > total ? total : per;
   if (per > sla::kRotaryUnroll) per = per / sla::kRotaryUnroll * sla::kRotaryUnroll;
   a.heads_per_block = static_cast<int>(per);
