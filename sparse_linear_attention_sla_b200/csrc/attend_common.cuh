@@ -21,6 +21,8 @@ struct AttendArgs {
   int units;
   int waves;    // units c, c + gridDim.x, ... that CTA c takes whole, this many of them
   int uniform;  // every unit has the same number of steps
+  int spans;    // not 0: units are taken whole and longest first, |spans| of them to a head, of which the last
+                // (below 0: the first) is the longest
   int4* meta;   // [gridDim.x] what attend_join_kernel / attend_sum_kernel join (null: nothing is cut)
 };
 
@@ -76,9 +78,14 @@ struct AttendWork {
   __device__ __forceinline__ bool next(const AttendArgs& a, const Steps& steps, int& u_, int& lo, int& hi, int& n,
                                        int& to) {
     if (k < a.waves) {
-      u_ = blockIdx.x + k * gridDim.x;
+      // Longest first: every other wave runs backwards, so that long units meet short ones.
+      u_ = k * gridDim.x + (a.spans && (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       ++k;
       if (u_ >= a.units) return false;
+      if (a.spans) {
+        const int n_spans = abs(a.spans), heads = a.units / n_spans, rank = u_ / heads;
+        u_ = u_ % heads * n_spans + (a.spans > 0 ? n_spans - 1 - rank : rank);
+      }
       lo = 0;
       hi = n = to = max(1, steps(u_));
       return true;
