@@ -75,6 +75,8 @@ SHAPES = [
     (1, 3, 3, 128, 777),    # the most queries of one tile
     (40, 4, 2, 130, 130),   # more units than SMs
     (2, 6, 2, 130, 700),    # tiles of three heads and 42 queries
+    (2, 40, 40, 500, 500),  # causal: whole units, longest first, in waves of both directions
+    (3, 36, 12, 700, 650),  # the same with more queries than keys and shared key heads
     (1, 10, 2, 200, 333),   # tiles of five heads and 25 queries where that makes fewest, or equally many and causal
 ]
 
