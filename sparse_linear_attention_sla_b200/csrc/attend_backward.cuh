@@ -753,15 +753,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return warp_wait(bar, parity, a.err, &abort_flag);
     };
+    // The next unit, and its rows' statistics, which are on their way while the last unit's rows are written (cross
+    // attention over 512 keys, forward and backward: 582.6 us without, 575.1).
+    float nl_next = 0.f, nd_next = 0.f;
+    auto look = [&]() -> bool {
+      if (!items.get(ni++, item, a.err, &abort_flag)) return false;
+      const DqItem w(item);
+      if (!w.stop()) {
+        const size_t at = (static_cast<size_t>(w.b) * a.H + w.h) * f.pad + w.row0 + r;
+        nl_next = f.nlse[at];
+        nd_next = f.ndelta[at];
+      }
+      return true;
+    };
+    ok = look();
     while (ok) {
-      if (!(ok = items.get(ni++, item, a.err, &abort_flag))) break;
       const DqItem w(item);
       if (w.stop()) break;
       const int n = w.n;
       const int row = w.row0 + r;
       const int end = attend_key_end(a, w.len, row);
-      const size_t at = (static_cast<size_t>(w.b) * a.H + w.h) * f.pad + row;
-      const float nl = f.nlse[at], nd = f.ndelta[at];
+      const float nl = nl_next, nd = nd_next;
       const uint64_t nl2 = f2_make(nl, nl);
       uint64_t nd2 = f2_make(nd, nd);
       for (int j = 0; j < n; ++j, ++it) {
@@ -801,7 +813,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ++ne;
           const float delta = (buffer[0][r] + buffer[1][r]) + (buffer[2][r] + buffer[3][r]);
           nd2 = f2_make(-delta, -delta);
-          if (quarter == 0) f.ndelta[at] = -delta;
+          if (quarter == 0) f.ndelta[(static_cast<size_t>(w.b) * a.H + w.h) * f.pad + row] = -delta;
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -814,7 +826,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&t_full[it & 1]);
       }
-      if (!ok) break;
+      if (!ok || !(ok = look())) break;
       if (n > 0) {
         if (!(ok = wait(&acc_full, nu & 1))) break;
         tc_fence_after();

@@ -174,7 +174,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 }
 
 // The unit that a CTA works on, as its scheduler warp passes it to the other warps.
-struct AttendItem {
+struct __align__(16) AttendItem {
   int v[12];
 };
 
