@@ -14,7 +14,8 @@
 // delta is taken from out as it was given, in bf16 and with P rounded. Over many keys that is no matter; of two keys'
 // gradients it would be half of the error (0.0054 instead of 0.0024 of their norm, in bf16). Where a
 // sequence's keys fit one tile, the dQ kernel has a row's P and dP at hand and forms delta = sum_j P dP
-// itself, for the dK / dV kernel too, which then runs after it.
+// itself, for the dK / dV kernel too, which then runs after it. The first queries of longer causal sequences, which
+// see no more keys than one tile's, have it so for dQ alone: the dK / dV kernel would have to wait.
 //
 // P and T are rounded to bf16 for the tensor cores (by at most 2^-8 of each value); S, dP,
 // delta, lse and every sum are fp32. Rows without keys have lse = -inf: their P is 0, and
@@ -534,7 +535,7 @@ __device__ __forceinline__ DqUnit dq_unit(const AttendArgs& a, int u, bool recor
 }
 
 struct DqItem {
-  int b, h, row0, len, lo, n, slot, exact;  // exact: one key tile, delta is formed here
+  int b, h, row0, len, lo, n, slot, exact;  // exact: one key tile, delta is formed here (2: and written)
   __device__ __forceinline__ explicit DqItem(const AttendItem& i)
       : b(i.v[0]), h(i.v[1]), row0(i.v[2]), len(i.v[3]), lo(i.v[4]), n(i.v[5]), slot(i.v[6]),
         exact(i.v[7]) {}
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       while (ok && work.next(a, look, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
         item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n),
-                f.dq_first && w.len <= kTile};
+                w.tiles != 1 ? 0 : f.dq_first && w.len <= kTile ? 2 : 1};
         ok = items.put(ni++, item, a.err, &abort_flag);
       }
       item.v[0] = -1;
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ++ne;
           const float delta = (buffer[0][r] + buffer[1][r]) + (buffer[2][r] + buffer[3][r]);
           nd2 = f2_make(-delta, -delta);
-          if (quarter == 0) f.ndelta[(static_cast<size_t>(w.b) * a.H + w.h) * f.pad + row] = -delta;
+          if (w.exact == 2 && quarter == 0) f.ndelta[(static_cast<size_t>(w.b) * a.H + w.h) * f.pad + row] = -delta;
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {

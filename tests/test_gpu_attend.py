@@ -184,6 +184,20 @@ def test_gradients_of_few_keys(cuda_device, Nq, Nk, lens, D):
         assert float((got.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 * math.sqrt(2 / 3)
 
 
+def test_causal_dq_of_first_queries(cuda_device):
+    """The first 128 queries of a causal sequence have their delta from P and dP: their dq is the one that they have
+    alone, within the roundings of T and of dq itself (see test_gradients_of_few_keys). Row 0 sees one key: its
+    dq is 0 but for rounding."""
+    q, k, v, dO = _make(5, 1, 2, 1, 400, 400, 128, cuda_device)
+    out, lse = binding.attend(q, k, v, causal=True)
+    dq = binding.attend_backward(q, k, v, out, lse, dO, causal=True)[0]
+    s = lambda x, n: x[:, :, :n].contiguous()  # noqa: E731
+    short = binding.attend_backward(s(q, 128), s(k, 128), s(v, 128), s(out, 128), s(lse, 128), s(dO, 128), causal=True)[0]
+    assert torch.equal(dq[:, :, :128], short)
+    ref = oa.gradients(q, k, v, dO, causal=True)[0][:, :, 1:128]
+    assert (dq[:, :, 1:128].double() - ref).norm() <= 2.0 ** -8 * math.sqrt(2 / 3) * ref.norm()
+
+
 def test_nan_gradients_stay_out_of_rows_without_a_part(cuda_device):
     """NaN in dO spreads to what it enters; keys behind a length and queries without keys get exact zeros."""
     for Nq, Nk, n, causal in ((40, 300, 130, False), (300, 200, 60, True)):
