@@ -413,7 +413,8 @@ sla_status sla_rotary_backward(const sla_rotary_spec* spec, int B, int Hq, int H
  *                   sequence's length may hold anything, NaN included; their gradients are 0.
  *                   A length outside [0, Nk] is taken as the nearer end and reported by sla_check
  *   causal          1: query i sees the keys j <= i + len - Nq (the last query sees the last key)
- * A query that sees no key gives out = 0, lse = -inf and a zero gradient.
+ * A query that sees no key gives out = 0, lse = -inf and a zero gradient. A query one of whose scores is
+ * NaN or +infinity gives NaN in out and lse, and makes its own gradient and those of every key it sees NaN.
  * D is 64 or 128; Nq, Nk at most 2^24; scale > 0.
  */
 typedef struct {

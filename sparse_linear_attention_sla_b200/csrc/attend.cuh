@@ -11,7 +11,8 @@
 // m is the row maximum of the first tile with a visible key and moves (acc and l rescaled)
 // only when a tile's sum passes 2^20, as in the sparse kernels. P is rounded to bf16 for the
 // tensor cores (each p by at most 2^-8 of itself, independently; l sums the unrounded p);
-// S, acc, m and l are fp32. A row without keys gives out = 0 and lse = -inf.
+// S, acc, m and l are fp32. A row without keys gives out = 0 and lse = -inf; a NaN among a row's scores makes
+// both NaN, whole or in parts.
 //
 // One persistent CTA per SM, 384 threads. A tile is at most 128 rows, `heads` query heads that share a
 // key head x `tokens` queries. A unit is, with more than 128 queries, two neighbouring tiles A and B
@@ -462,8 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n > 0 && !(ok = wait(&pv_done[x][(ns - 1) & 1], ((ns - 1) >> 1) & 1))) break;
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+      // A row that saw no key has l = 0; a NaN in l is none of those, it goes on into out and lse.
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
       const size_t part_row = narrow ? static_cast<size_t>(w.slot) * kTile + r
                                      : static_cast<size_t>(w.slot) * 2 * kTile + x * kTile + r;
       __nv_bfloat16* const out = f.out.p + w.b * f.out.sb + h * f.out.sh + i * f.out.sn;
@@ -547,14 +549,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       y[p] = v[1];
     }
     const float top = fmaxf(fmaxf(fmaxf(lse2[0], lse2[1]), fmaxf(lse2[2], lse2[3])), m);
-    if (top == -INFINITY) continue;  // no part has seen a key yet
-    const float g = exp2f(m - top);
+    // No part has seen a key yet: every weight is 0. (The maximum passes a part's NaN over; its weight does not.)
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float g = exp2f(m - ref);
     sum *= g;
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[q] *= g;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const float e = exp2f(lse2[p] - top);
+      const float e = exp2f(lse2[p] - ref);
       const float v[8] = {x[p].x, x[p].y, x[p].z, x[p].w, y[p].x, y[p].y, y[p].z, y[p].w};
       sum += e;
 #pragma unroll
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
     m = top;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t o[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       make_uint4(o[0], o[1], o[2], o[3]);
   if (c == 0)
     f.lse[(static_cast<size_t>(w.b) * a.H + h) * a.Nq + i] =
-        sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace sla
