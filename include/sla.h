@@ -415,6 +415,9 @@ sla_status sla_rotary_backward(const sla_rotary_spec* spec, int B, int Hq, int H
  *   causal          1: query i sees the keys j <= i + len - Nq (the last query sees the last key)
  * A query that sees no key gives out = 0, lse = -inf and a zero gradient. A query one of whose scores is
  * NaN or +infinity gives NaN in out and lse, and makes its own gradient and those of every key it sees NaN.
+ * out and lse hold for finite scores of any size. The gradients recompute e^(score - lse) from the fp32 lse,
+ * whose rounding is a factor of up to e^(2^-23 |lse|) of a row's probabilities: past |lse| = 2^15 that is more
+ * than bf16's own rounding, and past 2^29 gradients may be infinite or NaN.
  * D is 64 or 128; Nq, Nk at most 2^24; scale > 0.
  */
 typedef struct {

@@ -130,6 +130,20 @@ __device__ __forceinline__ void mask_cols32(uint32_t (&x)[32], int key0, int end
     if (key0 + c >= end) x[c] = __float_as_uint(-INFINITY);
 }
 
+// A row's reference from its largest score `top` so far: m = top sc, and p = 2^(s mul - ref) of a score s, in one
+// FMA, with mul = sc and ref = m. The FMA keeps what m lost in its own rounding, a factor of the whole row until
+// half a step of m passes the exponent's range (128 at |m| = 2^32). From 2^30 on mul is the power of two below
+// sc, so that ref = top mul is exact and the largest p is 1; scores that differ lie 64 apart there by their own
+// rounding, so that the others' p, 2^-64 at most, is below 2^-32 either way.
+constexpr float kExactRef = 0x1p30f;
+
+__device__ __forceinline__ void attend_refer(float top, float sc, float& m, float& mul, float& ref) {
+  m = top * sc;
+  const bool exact = fabsf(m) >= kExactRef && fabsf(m) < INFINITY;
+  mul = exact ? __uint_as_float(__float_as_uint(sc) & 0x7F800000u) : sc;
+  ref = top * mul;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -358,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = lane_addr + x * 128, o_addr = lane_addr + ACC + x * 128;
     const float sc = a.scale_log2;
-    const uint64_t sc2 = f2_make(sc, sc);
     uint32_t ni = 0, ns = 0, nu = 0, nbb = 0;  // items; blocks of x; narrow: units with tiles of B, and their blocks
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(bar, parity, a.err, &abort_flag); };
@@ -380,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = row.h, i = row.i, n = row.n, other = row.other, end = row.end, end_min = row.end_min;
       const bool real = row.real;
       float m = -INFINITY, l = 0.f;
+      float mul = sc, ref = -INFINITY;  // p = 2^(s mul - ref): see attend_refer
       for (int t = 0; t < n; ++t, ++ns) {
         const uint32_t b = ns & 1, sb = s_addr + b * 64;
         if (!(ok = wait(&s_full[x][b], (ns >> 1) & 1))) break;
@@ -394,21 +408,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           mask_cols32(s[1], key0 + 32, end);
         }
         if (__any_sync(0xffffffffu, m == -INFINITY)) {
-          const float top = row_max64(s[0], s[1]) * sc;
-          if (m == -INFINITY) m = top;
+          const float top = row_max64(s[0], s[1]);
+          if (m == -INFINITY) attend_refer(top, sc, m, mul, ref);
         }
         uint32_t pk[32];
         auto exponentials = [&]() -> float {
-          const float ref = m == -INFINITY ? 0.f : m;  // no key seen yet: every s is -inf
-          const uint64_t part = exp2_block(s[0], s[1], pk, sc2, f2_make(-ref, -ref));
+          const float r = ref == -INFINITY ? 0.f : ref;  // no key seen yet: every s is -inf
+          const uint64_t part = exp2_block(s[0], s[1], pk, f2_make(mul, mul), f2_make(-r, -r));
           return f2_lo(part) + f2_hi(part);
         };
         float sum = exponentials();
         if (__any_sync(0xffffffffu, sum > kRefMoveSum)) {
           // Only the rows that passed move: a row's bits depend on nothing but its own scores (rows of
           // the tile that are no query hold whatever shared memory held).
-          const float top = sum > kRefMoveSum ? fmaxf(m, row_max64(s[0], s[1]) * sc) : m;
-          const float g = m == -INFINITY ? 1.f : fast_exp2(m - top);
+          const float top = row_max64(s[0], s[1]), m_old = m, mul_old = mul, ref_old = ref;
+          if (sum > kRefMoveSum && top * sc >= m) attend_refer(top, sc, m, mul, ref);
+          const float g = m == -INFINITY ? 1.f : fast_exp2(mul == mul_old ? ref_old - ref : m_old - m);
           if (t > 0) {  // S_t was seen, so of the products only the last can be open
             if (!(ok = wait(&pv_done[x][b ^ 1], ((ns - 1) >> 1) & 1))) break;
             tc_fence_after();
@@ -423,7 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           l *= g;
-          m = top;
           sum = exponentials();
         }
         l += sum;

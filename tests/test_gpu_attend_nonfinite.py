@@ -1,5 +1,5 @@
-"""Dense attention on inputs that are not finite: what a NaN or an infinity enters is not finite, everything else is as
-it is without it, whether a call's units are whole or cut into parts."""
+"""Dense attention on inputs that are not finite, and on finite scores of any size: what a NaN or an infinity enters is
+not finite, everything else is as it is without it, whether a call's units are whole or cut into parts."""
 
 import math
 
@@ -91,3 +91,56 @@ def test_infinite_scores(cuda_device, Nq, Nk, lens):
     out, lse = binding.attend(q, k, v, kv)
     want, wlse = binding.attend(q, hidden, v, kv)
     assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+# Magnitudes of the scores: below and above where half a step of the largest, in base 2, is 128.
+SIZES = (2.0 ** 24, 2.0 ** 29, 2.0 ** 31, 2.0 ** 33, 2.0 ** 36, 1e20, 1e37)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("Nq, Nk", [(64, 128), (300, 300), (1, 4000), (300, 1500)])
+def test_finite_scores_of_any_size(cuda_device, Nq, Nk, sign):
+    """Scores c k_j of distinct k_j, exact in fp32: the row is one-hot, out the value of the largest score and lse that
+    score, off by the rounding of the score, of the scale and of two products (2^-22 of it), wherever it lies and
+    whatever the rows beside it hold."""
+    q, k, v, _ = _make(7 * Nq + Nk, Nq, Nk, cuda_device)
+    g = torch.Generator().manual_seed(Nq + Nk)
+    rows = min(Nq, len(SIZES) * 3)
+    for b in range(B):
+        for h in range(HK):  # distinct bf16 numbers from -1 up and from 1 down, in some order
+            n = torch.randperm(Nk, generator=g)
+            size = (0x3f80 - n // 2).to(torch.int16).view(torch.bfloat16)
+            k[b, h, :, 0] = torch.where(n % 2 == 0, size, -size).to(cuda_device)
+    q[..., 0] = 0
+    want, wlse = binding.attend(q, k, v)
+    for r in range(rows):
+        q[:, :, r] = 0
+        q[:, :, r, 0] = sign * SIZES[(r + Nk) % len(SIZES)]
+    out, lse = binding.attend(q, k, v)
+    assert torch.equal(out[:, :, rows:], want[:, :, rows:]) and torch.equal(lse[:, :, rows:], wlse[:, :, rows:])
+    first = k[..., 0].double()
+    at = (first * sign).argmax(-1)  # [B, HK]
+    for b in range(B):
+        for h in range(H):
+            best = at[b, h // (H // HK)]
+            assert torch.equal(out[b, h, :rows], v[b, h // (H // HK), best].expand(rows, D)), (b, h)
+            ref = q[b, h, :rows, 0].double() * first[b, h // (H // HK), best] / D ** 0.5
+            assert ((lse[b, h, :rows].double() - ref).abs() <= 2.0 ** -22 * ref.abs()).all()
+
+
+def test_references_that_leave_and_enter_the_largest_sizes(cuda_device):
+    """The first keys' scores are huge and negative, then ordinary; ordinary, then huge; equal huge ones share a row."""
+    q, k, v, _ = _make(77, 200, 1000, cuda_device)
+    q[..., 0], k[..., 0] = 1e18, 0
+    low = k.clone()
+    low[:, :, :300, 0] = -1e18
+    out, lse = binding.attend(q, low, v)
+    want, wlse = binding.attend(q, k[:, :, 300:], v[:, :, 300:])
+    tol = 2.0 ** -7 * v.float().abs().max()  # of each call: a rounding of P and one of out, by 2^-8 of |v| at most
+    assert ((out.float() - want.float()).abs() <= 2 * tol).all()
+    assert ((lse - wlse).abs() <= 2.0 ** -20 * (1 + wlse.abs())).all()
+    k[:, :, 500, 0] = k[:, :, 900, 0] = 1e18
+    k[:, :, [500, 900], 1:] = 0
+    out, lse = binding.attend(q, k, v)
+    mean = (v[:, :, 500].float() + v[:, :, 900].float()).repeat_interleave(H // HK, 1)[:, :, None] / 2
+    assert ((out.float() - mean).abs() <= 2.0 ** -8 * mean.abs()).all()
