@@ -630,7 +630,7 @@ def _check_apart(name, y, *others):
 def _interleaved(x, y):
     """x and y are slices of one buffer that never meet: every step between rows is a multiple of the smallest, and
     within that one their row blocks lie apart."""
-    steps = [s * t.element_size() for t in (x, y) for n, s in zip(t.shape[:3], t.stride()) if n > 1]
+    steps = [s * t.element_size() for t in (x, y) for n, s in zip(t.shape[:3], t.stride()) if n > 1 and s > 0]
     for period in sorted(set(steps)):
         def block(t):  # bytes of the dimensions that stay within the period
             return (sum((n - 1) * s for n, s in zip(t.shape, t.stride()) if s * t.element_size() < period) + 1) \
