@@ -365,7 +365,8 @@ enum { SLA_BF16 = 0, SLA_F32 = 1 };
 
 /* A [B, H, N, D] tensor on the device: channels contiguous, the other strides in elements
  * and multiples of 16 bytes (a stride is not read where its extent is 1), ptr 16-byte
- * aligned. So a projection's [B, N, H, D] output is passed as it lies. */
+ * aligned. So a projection's [B, N, H, D] output is passed as it lies. An output's strides, in ascending order,
+ * each pass what lies within them, so that no two of its rows share memory; others are refused. */
 typedef struct {
   void* ptr;
   int64_t stride_b, stride_h, stride_n;

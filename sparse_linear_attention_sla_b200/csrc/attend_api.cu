@@ -225,6 +225,13 @@ sla_status check_operand(const char* name, const sla_tensor* t, int B, int heads
   return SLA_OK;
 }
 
+// The same for an output.
+sla_status check_output(const char* name, const sla_tensor* t, int B, int heads, int N, int D) {
+  SLA_TRY(check_operand(name, t, B, heads, N));
+  if (!rows_apart(t, B, heads, N, D)) return fail(SLA_ERR_INVALID_ARG, "%s has rows that overlap each other", name);
+  return SLA_OK;
+}
+
 // The queries as (channel, token, head of the group, key head, sequence): boxes of `tokens` rows of
 // `heads` heads.
 sla_status query_map(CUtensorMap* m, const sla_tensor* t, const sla_attend_problem& p, int tokens, int heads) {
@@ -347,7 +354,7 @@ sla_status sla_attend(const sla_attend_problem* p, const sla_tensor* q, const sl
   SLA_TRY(check_operand("q", q, p->B, p->H, p->Nq));
   SLA_TRY(check_operand("k", k, p->B, p->Hk, p->Nk));
   SLA_TRY(check_operand("v", v, p->B, p->Hk, p->Nk));
-  SLA_TRY(check_operand("out", out, p->B, p->H, p->Nq));
+  SLA_TRY(check_output("out", out, p->B, p->H, p->Nq, p->D));
   SLA_TRY(check_lens(kv_lens));
   if (!lse || reinterpret_cast<uintptr_t>(lse) % 4) return fail(SLA_ERR_INVALID_ARG, "lse must be non-NULL and 4-byte aligned");
   AttendSpace s;
@@ -381,9 +388,9 @@ sla_status sla_attend_backward(const sla_attend_problem* p, const sla_tensor* q,
   SLA_TRY(check_operand("v", v, p->B, p->Hk, p->Nk));
   SLA_TRY(check_operand("out", out, p->B, p->H, p->Nq));
   SLA_TRY(check_operand("dO", dO, p->B, p->H, p->Nq));
-  SLA_TRY(check_operand("dq", dq, p->B, p->H, p->Nq));
-  SLA_TRY(check_operand("dk", dk, p->B, p->Hk, p->Nk));
-  SLA_TRY(check_operand("dv", dv, p->B, p->Hk, p->Nk));
+  SLA_TRY(check_output("dq", dq, p->B, p->H, p->Nq, p->D));
+  SLA_TRY(check_output("dk", dk, p->B, p->Hk, p->Nk, p->D));
+  SLA_TRY(check_output("dv", dv, p->B, p->Hk, p->Nk, p->D));
   SLA_TRY(check_lens(kv_lens));
   if (!lse || reinterpret_cast<uintptr_t>(lse) % 4) return fail(SLA_ERR_INVALID_ARG, "lse must be non-NULL and 4-byte aligned");
   AttendSpace s;

@@ -45,6 +45,28 @@ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 inline bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
 
+// Whether the rows of D elements of an output [B, heads, N, D] lie apart: in ascending order, each stride over
+// an extent above 1 passes what lies within it. (Rows that meet would be written by several blocks at once, and
+// in place read by some after others have written them.)
+inline bool rows_apart(const sla_tensor* t, int B, int heads, int N, int D) {
+  const int64_t given[3] = {t->stride_b, t->stride_h, t->stride_n};
+  const int extent[3] = {B, heads, N};
+  unsigned __int128 span = D, last = 0;
+  for (int done = 0; done < 3; ++done) {  // the smallest stride not yet taken
+    int at = -1;
+    unsigned __int128 stride = 0;
+    for (int d = 0; d < 3; ++d) {
+      const unsigned __int128 s = static_cast<unsigned __int128>(given[d] < 0 ? -static_cast<__int128>(given[d]) : given[d]) * 4 + d;
+      if (extent[d] > 1 && (done == 0 || s > last) && (at < 0 || s < stride)) at = d, stride = s;
+    }
+    if (at < 0) return true;
+    last = stride;
+    if (stride / 4 < span) return false;
+    span += stride / 4 * (extent[at] - 1);
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ TMA descriptors
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -102,6 +102,8 @@ sla_status rotate(const sla_rotary_spec* spec, const RotaryCall& c, int in_type,
     if (c.heads[w] == 0) continue;
     SLA_TRY(check_tensor(names[w][0], c.in[w], in_type, c.B, c.heads[w], c.N));
     SLA_TRY(check_tensor(names[w][1], c.out[w], out_type, c.B, c.heads[w], c.N));
+    if (!rows_apart(c.out[w], c.B, c.heads[w], c.N, c.D))
+      return fail(SLA_ERR_INVALID_ARG, "%s has rows that overlap each other", names[w][1]);
     a.t[w] = {c.in[w]->ptr,      c.out[w]->ptr,      c.in[w]->stride_b,  c.in[w]->stride_h, c.in[w]->stride_n,
               c.out[w]->stride_b, c.out[w]->stride_h, c.out[w]->stride_n};
   }
