@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kScheduleWarp) {
     if (lane == 0) {
       uint32_t ni = 0;
-      int u, lo, hi, n, to;
+      int u, lo, hi, n, to, longest = 0;  // steps of the longest item
       bool ok = true;
       AttendUnit w;  // the unit that `next` looked at last, which is the one it gives
       const auto look = [&](int v) {
@@ -217,10 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         note_part(a, work, u, lo, hi, n, to);
         item = {w.b, w.h, w.hk, w.row0, w.len, lo, w.count(narrow, 0, lo, hi), w.count(narrow, 1, lo, hi),
                 part_slot(lo, hi, n)};
-        ok = items.put(ni++, item, a.err, &abort_flag);
+        longest = max(longest, hi - lo);
+        ok = items.put(ni++, item, longest, a.err, &abort_flag);
       }
       item.v[0] = -1;
-      if (ok) items.put(ni, item, a.err, &abort_flag);
+      if (ok) items.put(ni, item, longest, a.err, &abort_flag);
     }
     __syncwarp();
   } else if (warp == kProducerWarp) {

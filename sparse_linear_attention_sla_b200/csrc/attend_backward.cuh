@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == kScheduleWarp) {
     if (lane == 0) {
       uint32_t ni = 0;
-      int u, lo, hi, n, to;
+      int u, lo, hi, n, to, longest = 0;  // steps of the longest item
       bool ok = true;
       DkvUnit w;  // the unit that `next` looked at last, which is the one it gives
       const auto look = [&](int v) {
@@ -325,10 +325,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       while (ok && work.next(a, look, u, lo, hi, n, to)) {
         note_part(a, work, u, lo, hi, n, to);
         item = {w.b, w.hk, w.key0, w.len, w.first, w.tiles, w.dead, lo, hi, part_slot(lo, hi, n)};
-        ok = items.put(ni++, item, a.err, &sh.abort_flag);
+        longest = max(longest, hi - lo);
+        ok = items.put(ni++, item, longest, a.err, &sh.abort_flag);
       }
       item.v[0] = -1;
-      if (ok) items.put(ni, item, a.err, &sh.abort_flag);
+      if (ok) items.put(ni, item, longest, a.err, &sh.abort_flag);
     }
     __syncwarp();
   } else if (warp == kProducerWarp) {
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == kScheduleWarp) {
     if (lane == 0) {
       uint32_t ni = 0;
-      int u, lo, hi, n, to;
+      int u, lo, hi, n, to, longest = 0;  // steps of the longest item
       bool ok = true;
       DqUnit w;  // the unit that `next` looked at last, which is the one it gives
       const auto look = [&](int v) {
@@ -620,10 +621,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         note_part(a, work, u, lo, hi, n, to);
         item = {w.b, w.h, w.row0, w.len, lo, w.tiles > 0 ? hi - lo : 0, part_slot(lo, hi, n),
                 w.tiles != 1 ? 0 : f.dq_first && w.len <= kTile ? 2 : 1};
-        ok = items.put(ni++, item, a.err, &abort_flag);
+        longest = max(longest, hi - lo);
+        ok = items.put(ni++, item, longest, a.err, &abort_flag);
       }
       item.v[0] = -1;
-      if (ok) items.put(ni, item, a.err, &abort_flag);
+      if (ok) items.put(ni, item, longest, a.err, &abort_flag);
     }
     __syncwarp();
   } else if (warp == kProducerWarp) {

@@ -173,6 +173,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort_flag));
 }
 
+// How long the scheduler waits for the longest unit so far, of `steps` steps, to end: a key tile's unit has up to 2^30
+// (query heads of a group x query tiles), and at 2.1 us a step (D = 128, 1.65 GHz) 960 thousand pass the limit of
+// every other wait, which is for one step. Four times that pace is waited for.
+constexpr uint64_t kStepWaitNs = 8400;
+__host__ __device__ constexpr uint64_t item_wait_ns(int steps) {
+  return SLA_WAIT_LIMIT_NS + kStepWaitNs * static_cast<uint64_t>(steps);
+}
+
 // The unit that a CTA works on, as its scheduler warp passes it to the other warps.
 struct __align__(16) AttendItem {
   int v[12];
@@ -193,10 +201,12 @@ struct ItemRing {
       mbar_init(&empty[s], READERS);
     }
   }
-  // By one thread.
-  __device__ __forceinline__ bool put(uint32_t i, const AttendItem& x, uint32_t* err, volatile int* abort_flag) {
+  // By one thread. A slot comes free when the readers take the unit in it, which is when they end the one before:
+  // no unit so far has had more than `steps` steps.
+  __device__ __forceinline__ bool put(uint32_t i, const AttendItem& x, int steps, uint32_t* err,
+                                      volatile int* abort_flag) {
     const uint32_t s = i % SLOTS, r = i / SLOTS;
-    if (r > 0 && !mbar_wait(&empty[s], (r - 1) & 1, err, abort_flag)) return false;
+    if (r > 0 && !mbar_wait_for(&empty[s], (r - 1) & 1, err, abort_flag, item_wait_ns(steps))) return false;
     item[s] = x;
     mbar_arrive(&full[s]);
     return true;

@@ -3,7 +3,7 @@
 // allocation, UMMA issue/commit, TMEM loads/stores).
 //
 // Every wait in this library is bounded: after SLA_WAIT_LIMIT_NS nanoseconds
-// (global timer) a wait gives up, records SLA_DEVERR_TIMEOUT in the device error
+// (global timer; more where a wait spans many steps of known number) a wait gives up, records SLA_DEVERR_TIMEOUT in the device error
 // word and reports failure, so a logic error shows up as an error status
 // instead of a hung GPU.
 #pragma once
