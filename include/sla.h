@@ -424,7 +424,7 @@ sla_status sla_rotary_backward(const sla_rotary_spec* spec, int B, int Hq, int H
 typedef struct {
   int B, H, Hk, Nq, Nk, D;
   int causal;  /* 0 or 1 */
-  float scale; /* finite, > 0; 1 / sqrt(D) is usual */
+  float scale; /* > 0, scale * log2(e) finite; 1 / sqrt(D) is usual */
 } sla_attend_problem;
 
 /* Workspace bytes of sla_attend / sla_attend_backward for p; 0 if p is invalid (sla_last_error). */

@@ -108,7 +108,8 @@ sla_status make_plan(const sla_attend_problem* p, bool has_lens, bool bwd, Atten
   if (p->H % p->Hk) return fail(SLA_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", p->H, p->Hk);
   if (p->D != 64 && p->D != 128) return fail(SLA_ERR_UNSUPPORTED, "D=%d not supported (64 or 128)", p->D);
   if (p->causal != 0 && p->causal != 1) return fail(SLA_ERR_INVALID_ARG, "causal must be 0 or 1");
-  if (!std::isfinite(p->scale) || !(p->scale > 0.f)) return fail(SLA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!std::isfinite(p->scale * 1.4426950408889634f) || !(p->scale > 0.f))  // as the kernels take it, in base 2
+    return fail(SLA_ERR_INVALID_ARG, "scale must be finite, in base 2 too, and > 0");
   if (p->Nq > (1 << 24) || p->Nk > (1 << 24)) return fail(SLA_ERR_UNSUPPORTED, "Nq, Nk must be at most 2^24");
   const long long BH = static_cast<long long>(p->B) * p->H, BHk = static_cast<long long>(p->B) * p->Hk;
   const long long qt = (p->Nq + kTile - 1) / kTile, kt = (p->Nk + kTile - 1) / kTile;

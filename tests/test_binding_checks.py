@@ -97,3 +97,11 @@ def test_expanded_outputs_are_refused(cuda_device):
     assert torch.equal(one, kept) and not rolling.any()
     got = binding.rotary(wide, None, spec)[0]  # as an input it repeats
     assert torch.equal(got, binding.rotary(wide.contiguous(), None, spec)[0])
+
+
+def test_a_scale_past_fp32_in_base_two_is_refused(lib):
+    for scale, status in ((2.3e38, 3), (2.4e38, 1), (3.4e38, 1)):  # 3: the workspace is missing
+        p = binding.AttendProblem(1, 2, 2, 8, 8, 64, 0, scale)
+        x = binding.Tensor(1 << 30, 2 * 8 * 64, 8 * 64, 64)
+        assert (lib.sla_workspace_size_attend(p) > 0) == (status == 3)
+        assert lib.sla_attend(p, x, x, x, None, x, 1 << 21, None, 0, None) == status
