@@ -11,7 +11,7 @@ __version__ = "0.1.0"
 
 _BINDING_NAMES = ("forward", "route", "kv_states", "check", "counts", "problem", "new_workspace",
                   "workspace_size", "version", "SlaError", "rotary_spec", "rotary", "rotary_backward", "attend",
-                  "attend_backward")
+                  "attend_backward", "attend_problem", "new_workspace_attend")
 
 
 def __getattr__(name):

@@ -105,3 +105,11 @@ def test_a_scale_past_fp32_in_base_two_is_refused(lib):
         x = binding.Tensor(1 << 30, 2 * 8 * 64, 8 * 64, 64)
         assert (lib.sla_workspace_size_attend(p) > 0) == (status == 3)
         assert lib.sla_attend(p, x, x, x, None, x, 1 << 21, None, 0, None) == status
+
+
+def test_the_package_gives_every_call_of_rotary_and_attend():
+    import sparse_linear_attention_sla_b200 as package
+
+    for name in ("rotary_spec", "rotary", "rotary_backward", "attend", "attend_backward", "attend_problem",
+                 "new_workspace_attend", "check"):
+        assert getattr(package, name) is getattr(binding, name)
