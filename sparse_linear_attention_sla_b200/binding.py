@@ -762,7 +762,8 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
     q [B,H,Nq,D], k and v [B,Hk,Nk,D] bf16 with contiguous channels and any other strides; Hk
     divides H. kv_lens: int32 [B] keys of each sequence (None: Nk). causal: query i sees the keys
     j <= i + len - Nq. scale: 1 / sqrt(D) if None. A query without keys gives 0 and lse = -inf.
-    ws: new_workspace_attend's, kept where a device-side error is to be asked for with check(ws)."""
+    ws: new_workspace_attend's, kept where a device-side error is to be asked for with check(ws): without one of
+    the caller's, a length outside [0, Nk] or a wait that ran out shows nowhere."""
     p, (B, H, Hk, Nq, Nk, D), dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
     if out is None:
         out, o = _new_heads(dev, B, H, Nq, D, torch.bfloat16)
@@ -777,7 +778,8 @@ def attend(q, k, v, kv_lens=None, causal=False, scale=None, out=None, ws=None):
 
 def attend_backward(q, k, v, out, lse, dO, kv_lens=None, causal=False, scale=None, ws=None):
     """sla_attend_backward: (dq [B,H,Nq,D], dk, dv [B,Hk,Nk,D]) bf16 of sum(dO * out), from attend's
-    out and lse of the same arguments. Equal calls give equal bits."""
+    out and lse of the same arguments. Equal calls give equal bits. ws: new_workspace_attend's with
+    backward=True; as for attend."""
     p, (B, H, Hk, Nq, Nk, D), dev, args = _attend_inputs(q, k, v, kv_lens, causal, scale)
     o = _check_heads("out", out, B, H, Nq, D, torch.bfloat16, dev)
     g = _check_heads("dO", dO, B, H, Nq, D, torch.bfloat16, dev)

@@ -31,9 +31,10 @@
 // turns: 4600 cycles.)
 // A row's epilogue takes about 4000 cycles of a unit (a block of 64 keys 1950): rows lie apart, and the code, run once
 // a unit, is not at hand. It runs in rounds of 32 channels, and the next unit is looked up while its last product runs
-// (cross attention over 512 keys: 193.7 us with rounds of 64 and the lookup after, 189.9 with 32, 184.0 so).
-// Measured: 16380 tokens of 12 heads 1545 to 1612 us (1.04 PFLOP/s at 1.65 GHz), 2 x 32760 over 512 and 77 keys 184
-// to 200, one token over 4 x 8 heads of up to 32760 keys 55 with the join.
+// (cross attention over 512 and 77 keys, in turn on one GPU: 193.7 us with rounds of 64 and the lookup after, 189.9
+// with 32, 184.0 so).
+// Measured, a call on several GPUs of the kind: 16380 tokens of 12 heads 1436 to 1612 us (1.04 PFLOP/s at 1.65 GHz),
+// 2 x 32760 over 512 and 77 keys 184 to 206, one token over 4 x 8 heads of up to 32760 keys 55 to 64 with the join.
 // Parts of units (see AttendWork) are fp32 rows divided by their own sum, with the sum's log2;
 // attend_join_kernel joins them.
 #pragma once

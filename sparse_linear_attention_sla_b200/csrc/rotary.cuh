@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
   // The block's frequencies, one for each pair of channels, then this thread's angles. Pairs of
   // neighbours lie in one thread; halves share theirs through the table of all tokens' pairs.
   // A frequency is held as its fraction of a turn in 64 bits (whole turns per step drop out, positions
-  // being whole), so an angle is one integer product, reduced by its overflow: off by at most 2^-33 of a
-  // turn plus |p| times the fp64 rounding of the frequency.
+  // being whole), so an angle is one integer product, reduced by its overflow. It is off by 2^-32 of a turn at most
+  // for the product's dropped bits, by 2^-26 for the fp32 argument of sincospif and by |p| times the fp64 rounding
+  // of the frequency.
   __shared__ uint2 freq[D / 2];
   __shared__ float2 table[HALVES ? TOKENS * (D / 2) : 1];
   const int turned_channels = a.first[a.n_axes];
